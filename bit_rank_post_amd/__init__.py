@@ -26,7 +26,9 @@ EXPORTS = ["tq_layer_create", "tq_upload_proj", "tq_upload_shared_expert",
            "tq_workspace_size", "tq_forward", "tq_forward_from_logits", "tq_forward_noalloc", "tq_layer_destroy", "tq_last_error",
            "tq_abi_version", "tq_layer_set_path", "tq_forward_path", "tq_debug_route", "tq_debug_dequant", "tq_debug_row_bound", "tq_router_topk",
            "tq_profile_enable", "tq_profile_read", "tq_pack_workspace_size", "tq_pack_proj",
-           "tq_calibrate_read"]
+           "tq_calibrate_read", "tq_group_gemm", "tq_group_gemm_dx", "tq_group_gemm_dw", "tq_fp8_gemm",
+           "tq_fp8_quant_rows", "tq_fp8_quant_blocks", "tq_norm_residual", "tq_norm_grad_workspace_size",
+           "tq_norm_residual_grad"]
 STAGES = ["route", "row_exponent", "column_stage_in", "gemm_in", "column_stage_down",
           "shared_expert", "gemm_down", "combine"]
 
@@ -63,6 +65,32 @@ class PackDesc(ctypes.Structure):
                 ("zeros", ctypes.c_void_p)]
 
 
+class GroupDesc(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("rows", ctypes.c_int32), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("act", ctypes.c_int32), ("off", ctypes.c_void_p),
+                ("src", ctypes.c_void_p), ("src_div", ctypes.c_int32), ("x_rows", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d", "stream_dtype", "act", "w_dtype", "gate")]
+                + [("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+                + [(n, Rows) for n in ("x", "b", "y", "n", "gate_v")]
+                + [(n, ctypes.c_void_p) for n in ("w_post", "w_next", "rstd_post", "rstd_next")])
+
+
+class NormGradDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d", "stream_dtype", "act", "w_dtype", "gate")]
+                + [("alpha", ctypes.c_float)]
+                + [(n, Rows) for n in ("y", "dy", "dn", "b", "gate_v", "dx", "db", "dgate")]
+                + [(n, ctypes.c_void_p) for n in ("w_post", "w_next", "rstd_post", "rstd_next",
+                                                  "dw_post", "dw_next")])
+
+
 _lib = None
 
 
@@ -95,6 +123,16 @@ def lib():
         L.tq_calibrate_read.argtypes = [vp, ctypes.c_size_t, vp, vp]
         L.tq_pack_workspace_size.argtypes = [ctypes.POINTER(PackDesc), ctypes.POINTER(sz)]
         L.tq_pack_proj.argtypes = [ctypes.POINTER(PackDesc), vp, sz, vp]
+        pg = ctypes.POINTER(GroupDesc)
+        L.tq_group_gemm.argtypes = [pg, vp, vp, vp, i32, vp]
+        L.tq_group_gemm_dx.argtypes = [pg, vp, vp, vp, i32, vp]
+        L.tq_group_gemm_dw.argtypes = [pg, vp, vp, vp, i32, vp]
+        L.tq_fp8_gemm.argtypes = [pg, vp, vp, vp, vp, vp, i32, vp]
+        L.tq_fp8_quant_rows.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp]
+        L.tq_fp8_quant_blocks.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+        L.tq_norm_residual.argtypes = [ctypes.POINTER(NormDesc), vp]
+        L.tq_norm_grad_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
+        L.tq_norm_residual_grad.argtypes = [ctypes.POINTER(NormGradDesc), vp, sz, vp]
         for name in EXPORTS:
             if name not in ("tq_last_error", "tq_abi_version"):
                 getattr(L, name).restype = i32
@@ -118,6 +156,18 @@ def _stream(stream):
         import torch
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+
+
+# The operators around a layer (defined in ops.py, offered here)
+_OPS = ("group_gemm", "group_gemm_dx", "group_gemm_dw", "fp8_gemm", "fp8_quant_rows",
+        "fp8_quant_blocks", "norm_residual", "norm_residual_grad")
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import ops       # needs torch, which the rest of this module does not
+        return getattr(ops, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def calibrate_read(buf, scratch, stream=None):

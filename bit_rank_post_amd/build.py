@@ -26,7 +26,8 @@ SOURCES = [("route.hip", "route", []), ("colproj.hip", "colproj", []),
            ("gemm_decode.hip", "gemm_decode", []), ("decode_stages.hip", "decode_stages", []),
            ("combine.hip", "combine", []), ("upload.hip", "upload", []),
            ("router.hip", "router", []), ("pack.hip", "pack", []), ("calib.hip", "calib", []),
-           ("tileq_host.cpp", "tileq_host", [])]
+           ("group_gemm.hip", "group_gemm", []), ("quant8.hip", "quant8", []), ("norm.hip", "norm", []),
+           ("tileq_host.cpp", "tileq_host", []), ("ops_host.cpp", "ops_host", [])]
 
 
 def hipcc():
@@ -102,15 +103,20 @@ def build_asan() -> str:
         build()
     os.makedirs(ASAN_DIR, exist_ok=True)
     cc = hipcc()
-    obj = os.path.join(ASAN_DIR, "tileq_host.o")
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
            "-Xarch_host", "-fno-sanitize-recover=undefined",
            "-Xarch_host", "-fno-omit-frame-pointer", "-g"]
-    cmd = [cc] + flags() + san + ["-x", "hip", "-c", os.path.join(CSRC, "tileq_host.cpp"), "-o", obj]
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("hipcc (sanitized host) failed:\n" + r.stdout.decode(errors="replace"))
-    objs = [obj] + [os.path.join(BUILD, n + ".o") for _, n, _ in SOURCES if n != "tileq_host"]
+    objs = []
+    for src, name, _ in SOURCES:
+        if not src.endswith(".cpp"):
+            objs.append(os.path.join(BUILD, name + ".o"))
+            continue
+        obj = os.path.join(ASAN_DIR, name + ".o")
+        objs.append(obj)
+        cmd = [cc] + flags() + san + ["-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError("hipcc (sanitized host) failed:\n" + r.stdout.decode(errors="replace"))
     tmp = ASAN_LIB + ".tmp"
     r = subprocess.run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs,
                        stdout=subprocess.PIPE, stderr=subprocess.STDOUT)

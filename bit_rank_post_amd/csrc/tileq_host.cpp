@@ -81,6 +81,8 @@ struct tq_layer {
 };
 
 namespace tq {
+void set_last_error(const char* text) { g_err = text; }
+
 // Compute units of the current device (cached per device id; concurrent
 // first calls store the same value).
 int device_cus() {

@@ -48,6 +48,9 @@ struct SharedDev {
   void* wd;       // [d_model][d_ff] f16
 };
 
+// text of tq_last_error() on this thread (tileq_host.cpp)
+void set_last_error(const char* text);
+
 // ---- routing --------------------------------------------------------------
 struct RouteArgs {
   const int* ids;                // [T][k]; written by the router first when logits is set

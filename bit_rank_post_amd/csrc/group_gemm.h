@@ -27,7 +27,7 @@ struct GroupArgs {
   void* out;                     // Y [rows][ldo], DX [rows][ldo], DW [groups][d_out][d_in]
   long ldx, ldy, ldo;            // row strides in elements
   int out_dtype;                 // 0 f16, 1 bf16, 2 f32
-  int vec_out;                   // four neighbouring outputs may be stored at once
+  int vec_out;                   // eight neighbouring outputs may be stored as 16-byte words
   const float* xs;               // E4M3: [x_rows][ceil(d_in/128)] scales of x
   const float* ws;               // E4M3: [groups][ceil(d_out/128)][ceil(d_in/128)]
 };

@@ -19,7 +19,7 @@
 //
 // A workgroup computes an MT x NT tile of one group.  Stages of 128 bytes of
 // k per row (64 16-bit values, or 128 8-bit values) arrive by buffer loads
-// with the LDS destination in a ring of NBUF buffers.  Rows and k past the
+// with the LDS destination in rings of three stages of A and two of B.  Rows and k past the
 // group, the matrix or the row are never read: their lanes get an offset out
 // of the buffer's range, which loads zeros.  Groups are found from `off` in
 // the kernel (no host read back); offsets are clamped to 0 .. rows, so no
@@ -128,6 +128,22 @@ __device__ __forceinline__ void find_row_tile(const GroupArgs& a, int lane, int 
   *nrow = 0;
 }
 
+// The group with the i-th most rows (ties in order), so that long sums do not
+// start last; in plain order above 64 groups, where each one's share is small.
+__device__ __forceinline__ int longest_first(const GroupArgs& a, int lane, int i) {
+  if (a.groups > 64) return i;
+  int lo = 0, hi = -1;
+  if (lane < a.groups) group_span(a, lane, &lo, &hi);
+  const int n = hi - lo;                // -1 in lanes without a group
+  int rank = 0;
+  for (int l = 0; l < a.groups; ++l) {
+    const int m = __builtin_amdgcn_readlane(n, l);
+    rank += (m > n || (m == n && l < lane)) ? 1 : 0;
+  }
+  const uint64_t me = __ballot(lane < a.groups && rank == i);
+  return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)me) - 1);
+}
+
 // Work item of this workgroup: XCD x (workgroups x, x + 8, ...) takes one run
 // of consecutive items; inside a run, bands of 8 row tiles go over all m
 // tiles, so that the workgroups running together on an XCD share few rows of
@@ -145,28 +161,67 @@ __device__ __forceinline__ bool take_item(int ntile, int mtile, int* n, int* m) 
   return true;
 }
 
-__device__ __forceinline__ void store4(const GroupArgs& a, size_t at, const f32x4& v, int left) {
-  if (a.out_dtype == 2) {
-    float* p = reinterpret_cast<float*>(a.out) + at;
-    if (a.vec_out && left >= 4) *reinterpret_cast<f32x4*>(p) = v;
-    else
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) p[i] = v[i];
-    return;
-  }
-  uint16_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = a.out_dtype == 0 ? __builtin_bit_cast(uint16_t, (half_t)v[i])
-                            : __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+// Two neighbouring fragments of a column hold, in lane group g, outputs 4g ..
+// 4g+3 of 16 each.  Exchanged between the groups (rows of 16 lanes, two swaps a
+// register) group g holds 8 neighbours: 8g .. 8g+7 of the 32, and 64 bytes of
+// a 16-bit output row are written by one instruction.
+__device__ __forceinline__ void join_rows(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  const auto q = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
+  x = q[0];
+  y = q[1];
+  // pinned here: the exchange needs every lane, and must not move behind a
+  // caller's branch over the lanes that store
+  asm volatile("" : "+v"(x), "+v"(y));
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {a, b};
+  if constexpr (BF) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2v));
+}
+
+// outputs at .. at+7 of fragments v, w (joined), `left` of which exist
+template <bool BF>
+__device__ __forceinline__ void store8_16(const GroupArgs& a, size_t at, const f32x4& v, const f32x4& w, int left) {
+  uint32_t x0 = pack2<BF>(v[0], v[1]), x1 = pack2<BF>(v[2], v[3]);
+  uint32_t y0 = pack2<BF>(w[0], w[1]), y1 = pack2<BF>(w[2], w[3]);
+  join_rows(x0, y0);
+  join_rows(x1, y1);
+  if (left <= 0) return;
   uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + at;
-  if (a.vec_out && left >= 4)
-    *reinterpret_cast<u32x2*>(p) = u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
-  else
+  const u32x4 o = {x0, x1, y0, y1};
+  if (a.vec_out && left >= 8) {
+    *reinterpret_cast<u32x4*>(p) = o;
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) p[i] = h[i];
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+__device__ __forceinline__ void store8_32(const GroupArgs& a, size_t at, const f32x4& v, const f32x4& w, int left) {
+  uint32_t x[4], y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float vi = v[i], wi = w[i];
+    x[i] = __builtin_bit_cast(uint32_t, vi);
+    y[i] = __builtin_bit_cast(uint32_t, wi);
+    join_rows(x[i], y[i]);
+  }
+  if (left <= 0) return;
+  uint32_t* p = reinterpret_cast<uint32_t*>(a.out) + at;
+  if (a.vec_out && left >= 8) {
+    *reinterpret_cast<u32x4*>(p) = u32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<u32x4*>(p + 4) = u32x4{y[0], y[1], y[2], y[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = i < 4 ? x[i] : y[i - 4];
+  }
 }
 
 // One operand's tile of R rows (its m or n) in LDS.
@@ -183,7 +238,7 @@ struct Operand {
   static_assert(NLD * NTHR * 16 == BYTES, "loads split evenly");
 };
 
-template <typename T, int MODE, int MT, int NT, int WM, int WN, int NBUF>
+template <typename T, int MODE, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
   constexpr bool F8 = sizeof(T) == 1;
   constexpr bool AKC = MODE == GROUP_Y, BKC = MODE != GROUP_DW;
@@ -193,16 +248,19 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
   constexpr int FM = MT / WM / 16, FN = NT / WN / 16;
   typedef Operand<AKC, MT, NTHR> OA;
   typedef Operand<BKC, NT, NTHR> OB;
-  constexpr int SB = OA::BYTES + OB::BYTES;
-  static_assert(NBUF * SB <= 160 * 1024, "LDS budget");
+  static_assert(3 * OA::BYTES + 2 * OB::BYTES <= 160 * 1024, "LDS budget");
   static_assert(AKC || MT >= 128, "strided tile rows hold 8 pieces");
   static_assert(BKC || NT >= 128, "strided tile rows hold 8 pieces");
-  // one array per buffer: the compiler then knows that the loads in flight do
-  // not touch the buffer being read (with one array it waits for all of them)
-  __shared__ __attribute__((aligned(128))) char s0[SB];
-  __shared__ __attribute__((aligned(128))) char s1[SB];
-  __shared__ __attribute__((aligned(128))) char s2[NBUF > 2 ? SB : 16];
-  char* const ring[3] = {s0, s1, s2};
+  // One array per buffer: the compiler then knows that the loads in flight do
+  // not touch the buffer being read (with one array it waits for all of them).
+  // Three stages of A and two of B: 160 KB in a 256 x 256 tile.
+  __shared__ __attribute__((aligned(128))) char a0[OA::BYTES];
+  __shared__ __attribute__((aligned(128))) char a1[OA::BYTES];
+  __shared__ __attribute__((aligned(128))) char a2[OA::BYTES];
+  __shared__ __attribute__((aligned(128))) char b0[OB::BYTES];
+  __shared__ __attribute__((aligned(128))) char b1[OB::BYTES];
+  char* const ra_[3] = {a0, a1, a2};
+  char* const rb_[2] = {b0, b1};
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -215,11 +273,16 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
     mdim = a.d_in;
     ndim = a.d_out;
     const int mtile = (mdim + MT - 1) / MT, ntile = (ndim + NT - 1) / NT;
-    int it, m;
-    if (!take_item(a.groups * ntile, mtile, &it, &m)) return;
-    g = it / ntile;
-    n0 = (it - g * ntile) * NT;
-    m0 = m * MT;
+    // XCD x takes the m columns x, x + 8, ... of all groups in turn, each with
+    // all its n tiles: a group's work, which grows with its rows, is spread
+    // over the XCDs, and the workgroups together on an XCD share columns of x
+    const int li = blockIdx.x >> 3;
+    const int c = (li / ntile) * 8 + (blockIdx.x & 7);
+    if (c >= a.groups * mtile) return;
+    const int gi = c / mtile;
+    m0 = (c - gi * mtile) * MT;
+    n0 = (li % ntile) * NT;
+    g = longest_first(a, lane, gi);
     int lo, hi;
     group_span(a, g, &lo, &hi);
     row0 = __builtin_amdgcn_readfirstlane(lo);
@@ -295,82 +358,108 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
     sa = reinterpret_cast<const char*>(a.x) + (gather_k ? 0 : (size_t)row0 * lda) + (size_t)m0 * ES;
     sb = reinterpret_cast<const char*>(a.dy) + (size_t)row0 * ldb + (size_t)n0 * ES;
   }
-  // indices of the gathered k rows, requested one stage ahead of their loads
-  int sidx[OA::NLD];
+  // Gathered k rows: a load of this wave covers KR of them.  Their indices come
+  // by scalar loads (wave-uniform, counted apart from the loads in flight) a
+  // stage ahead of their use.
+  constexpr int KR = MODE == GROUP_DW ? 512 / MT : 1, NIDX = OA::NLD * KR;
+  int sidx[NIDX];
   auto want_rows = [&](int st) {
     if constexpr (MODE == GROUP_DW) {
-      if (gather_k) {
+      if (!gather_k) return;
+      const int k = st * KS + wave * NIDX;
+      if (k + NIDX <= K) {
 #pragma unroll
-        for (int i = 0; i < OA::NLD; ++i) {
-          int k, col;
-          strided(MT, i, OA::NLD, &k, &col);
-          const int r = st * KS + k;
-          sidx[i] = r < K ? a.src[row0 + r] : -1;
-        }
+        for (int q = 0; q < NIDX; ++q) sidx[q] = sload(a.src, row0 + k + q);
+      } else {
+#pragma unroll
+        for (int q = 0; q < NIDX; ++q) sidx[q] = k + q < K ? sload(a.src, row0 + k + q) : -1;
       }
     }
   };
 
-  auto issue = [&](int st, char* buf) {
+  // load i of A (B) of stage st
+  auto issue_a = [&](int st, char* buf, int i) {
     const int k0 = st * KS;
     const bool live = st < nstage;
+    char* to = buf + (wave * OA::NLD + i) * 1024;
     if constexpr (AKC) {
-#pragma unroll
-      for (int i = 0; i < OA::NLD; ++i) {
-        const int r = (wave * OA::NLD + i) * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ ((r >> 1) & 7);
-        const bool ok = live && k0 + c * (16 / ES) < K;
-        dma16(ra, buf + (wave * OA::NLD + i) * 1024, ok ? va[i] : OOB, live ? st * 128u : 0u);
-      }
+      const int r = (wave * OA::NLD + i) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const bool ok = live && k0 + c * (16 / ES) < K;
+      dma16(ra, to, ok ? va[i] : OOB, live ? st * 128u : 0u);
     } else {
-      const __amdgpu_buffer_rsrc_t r = make_rsrc(
-          live && !gather_k ? sa + (size_t)k0 * lda : sa, (uint32_t)OOB);
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(live && !gather_k ? sa + (size_t)k0 * lda : sa, (uint32_t)OOB);
+      int k, col;
+      strided(MT, i, OA::NLD, &k, &col);
+      bool ok = k0 + k < K && m0 + col < mdim;
+      int row = k;
+      if constexpr (MODE == GROUP_DW) {
+        if (gather_k) {
+          row = source_row(a, sidx[i * KR]);
 #pragma unroll
-      for (int i = 0; i < OA::NLD; ++i) {
-        int k, col;
-        strided(MT, i, OA::NLD, &k, &col);
-        bool ok = k0 + k < K && m0 + col < mdim;
-        int row = k;
-        if constexpr (MODE == GROUP_DW) {
-          if (gather_k) {
-            row = source_row(a, sidx[i]);
-            ok = ok && row >= 0;
+          for (int q = 1; q < KR; ++q) {
+            const int rq = source_row(a, sidx[i * KR + q]);
+            row = lane >= q * (64 / KR) ? rq : row;
           }
+          ok = ok && row >= 0;
         }
-        dma16(r, buf + (wave * OA::NLD + i) * 1024, ok ? (uint32_t)row * (uint32_t)lda + col * ES : OOB, 0);
       }
+      dma16(r, to, ok ? (uint32_t)row * (uint32_t)lda + col * ES : OOB, 0);
     }
-    char* bb = buf + OA::BYTES;
+  };
+  auto issue_b = [&](int st, char* buf, int i) {
+    const int k0 = st * KS;
+    const bool live = st < nstage;
+    char* to = buf + (wave * OB::NLD + i) * 1024;
     if constexpr (BKC) {
-#pragma unroll
-      for (int i = 0; i < OB::NLD; ++i) {
-        const int r = (wave * OB::NLD + i) * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ ((r >> 1) & 7);
-        const bool ok = live && k0 + c * (16 / ES) < K;
-        dma16(rb, bb + (wave * OB::NLD + i) * 1024, ok ? vb[i] : OOB, live ? st * 128u : 0u);
-      }
+      const int r = (wave * OB::NLD + i) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const bool ok = live && k0 + c * (16 / ES) < K;
+      dma16(rb, to, ok ? vb[i] : OOB, live ? st * 128u : 0u);
     } else {
       const __amdgpu_buffer_rsrc_t r = make_rsrc(live ? sb + (size_t)k0 * ldb : sb, (uint32_t)OOB);
-#pragma unroll
-      for (int i = 0; i < OB::NLD; ++i) {
-        int k, col;
-        strided(NT, i, OB::NLD, &k, &col);
-        const bool ok = k0 + k < K && n0 + col < ndim;
-        dma16(r, bb + (wave * OB::NLD + i) * 1024, ok ? (uint32_t)k * (uint32_t)ldb + col * ES : OOB, 0);
-      }
+      int k, col;
+      strided(NT, i, OB::NLD, &k, &col);
+      const bool ok = k0 + k < K && n0 + col < ndim;
+      dma16(r, to, ok ? (uint32_t)k * (uint32_t)ldb + col * ES : OOB, 0);
     }
-    want_rows(st + 1);
   };
+  auto issue_all = [&](int st, char* ab, char* bb) {
+    if (bb != nullptr) {
+#pragma unroll
+      for (int i = 0; i < OB::NLD; ++i) issue_b(st, bb, i);
+    }
+    if (ab != nullptr) {
+#pragma unroll
+      for (int i = 0; i < OA::NLD; ++i) issue_a(st, ab, i);
+    }
+  };
+  // Ring: A runs three stages ahead and B two, since 160 KB hold no third B: with
+  // both two ahead only one stage of loads is in flight (a buffer is free when
+  // the next stage has landed), and a stage then takes as long as a trip to
+  // memory.  Order of the loads: A0 B0 A1 B1 A2 | B2 A3 | B3 A4 | ...
+  want_rows(0);
+  issue_all(0, ra_[0], nullptr);
+  issue_all(0, nullptr, rb_[0]);
+  want_rows(1);
+  issue_all(1, ra_[1], nullptr);
+  issue_all(1, nullptr, rb_[1]);
+  want_rows(2);
+  issue_all(2, ra_[2], nullptr);
+  want_rows(3);
 
   // fragment f (16 rows) of an operand for half h of the stage
   const int kc_at = l16 * 128 + ((lg ^ ((l16 >> 1) & 7)) << 4);
   auto frag_kc = [&](const char* op, int f, int h) {
-    return *reinterpret_cast<const u32x4*>(op + f * 2048 + (kc_at ^ (h * 64)));
+    return *reinterpret_cast<const u32x4*>(op + f * 2048 + (opaque(kc_at) ^ (h * 64)));
   };
-  auto frag_st = [&](const char* op, int R, int f, int h) {
-    const int j = l16, k = 32 * h + 8 * lg + (j >> 2);
-    const int sw = (j >> 2) | ((lg & 1) << 2);
-    const char* p = op + k * (2 * R) + ((f ^ sw) << 5) + (j & 3) * 8;
+  // (strided: lane j = l16 of a group of 16 points at 4 elements of k row j/4
+  // and receives column j of the 4 rows; f0 is the wave's first fragment, a
+  // multiple of the fragments it reads, so that only i meets the swizzle)
+  const int st_k = 8 * lg + (l16 >> 2);
+  const int st_at = ((l16 >> 2) | ((lg & 1) << 2)) << 5 | (l16 & 3) << 3;
+  auto frag_st = [&](const char* op, int R, int f0, int i, int h) {
+    const char* p = op + (32 * h + st_k) * (2 * R) + ((((f0 + i) & ~7) << 5) + (opaque(st_at) ^ (((f0 + i) & 7) << 5)));
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 2 * R));
     return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -382,95 +471,177 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // 8-bit operands: scales of this lane's rows (one per n fragment) and of
-  // the wave's 128-output block, for k block st
-  const int nkb = (a.d_in + 127) >> 7;
-  const float* xsp[FN];
-  const float* wsp = nullptr;
   if constexpr (F8) {
+    // A stage is one k step of 128, one block of scales: the product of a row
+    // i of A's fragments with B comes out of the MFMA by itself and enters the
+    // sums times fl32(xs ws).  A's registers hold 4 rows: after row i they take
+    // row i + 4; in the last row, B's take the next stage.  The barrier
+    // (buffers of stage t free, stage t + 1 landed) follows row FM - 4.
+    static_assert(!F8 || (MT / WM <= 128 && 128 % (MT / WM) == 0), "wave inside a scale block");
+    constexpr int RA = FM < 4 ? FM : 4;           // rows of A in registers
+    constexpr int RB = FM - RA;                   // the row with the barrier
+    const int nkb = (a.d_in + 127) >> 7;
+    // scale of this lane's row for each n fragment, and of the wave's outputs
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(
+        a.src != nullptr ? a.xs : a.xs + (size_t)row0 * nkb, (uint32_t)OOB);
+    uint32_t xo[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int n = wn * (NT / WN) + 16 * j + l16;
-      int row = n < nrow ? row0 + n : -1;
-      if (row >= 0 && a.src != nullptr) row = source_row(a, a.src[row]);
-      xsp[j] = row >= 0 ? a.xs + (size_t)row * nkb : nullptr;
+      int row = n < nrow ? n : -1;
+      if (row >= 0 && a.src != nullptr) row = source_row(a, a.src[row0 + n]);
+      xo[j] = row >= 0 ? (uint32_t)row * nkb * 4u : OOB;
     }
-    // a wave's outputs lie in one block of 128
-    static_assert(!F8 || (MT / WM <= 128 && 128 % (MT / WM) == 0), "wave inside a scale block");
     const int ob = min((m0 + wm * (MT / WM)) >> 7, ((a.d_out + 127) >> 7) - 1);
-    wsp = a.ws + ((size_t)g * ((a.d_out + 127) >> 7) + ob) * nkb;
-  }
-
-  auto compute = [&](const char* buf, int st) {
-    const char* pa = buf + (AKC ? wm * (MT / WM) * 128 : 0);
-    const char* pb = buf + OA::BYTES + (BKC ? wn * (NT / WN) * 128 : 0);
-    if constexpr (F8) {
-      float sc[FN];
-      const float w = wsp[st];
+    const float* wsp = a.ws + ((size_t)g * ((a.d_out + 127) >> 7) + ob) * nkb;
+    float xs[2][FN], ws[2];
+    auto get_scales = [&](int st, int set) {      // (the last scale again past the end)
+      const int k = min(st, nstage - 1);
+      ws[set] = __builtin_bit_cast(float, sload(reinterpret_cast<const int*>(wsp), k));
 #pragma unroll
-      for (int j = 0; j < FN; ++j) sc[j] = xsp[j] != nullptr ? xsp[j][st] * w : 0.f;
-      u32x4 b0[FN], b1[FN];
+      for (int j = 0; j < FN; ++j)
+        xs[set][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, xo[j], k * 4u, 0));
+    };
+    u32x4 fa[RA][2], fb[FN][2];
+    auto get_a = [&](const char* op, int i) {
+      fa[i % RA][0] = frag_kc(op + wm * (MT / WM) * 128, i, 0);
+      fa[i % RA][1] = frag_kc(op + wm * (MT / WM) * 128, i, 1);
+    };
+    auto get_b = [&](const char* op, int j) {
+      fb[j][0] = frag_kc(op + wn * (NT / WN) * 128, j, 0);
+      fb[j][1] = frag_kc(op + wn * (NT / WN) * 128, j, 1);
+    };
+    get_scales(0, 0);
+    get_scales(1, 1);
+    wait_vm<0>();
+    bar_nofence();
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        b0[j] = frag_kc(pb, j, 0);
-        b1[j] = frag_kc(pb, j, 1);
-      }
+    for (int i = 0; i < RA; ++i) get_a(ra_[0], i);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const u32x4 a0 = frag_kc(pa, i, 0), a1 = frag_kc(pa, i, 1);
+    for (int j = 0; j < FN; ++j) get_b(rb_[0], j);
+    for (int t = 0; t < nstage; t += 6) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const f32x4 p = mfma_e4m3(a0, a1, b0[j], b1[j]);
+      for (int u = 0; u < 6; ++u) {
+        if (t + u >= nstage) break;
+        float sc[FN];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], sc[j], acc[i][j][v]);
+        for (int j = 0; j < FN; ++j) sc[j] = xs[u % 2][j] * ws[u % 2];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const f32x4 p = mfma_e4m3(fa[i % RA][0], fa[i % RA][1], fb[j][0], fb[j][1]);
+            if (i == FM - 1) get_b(rb_[(u + 1) % 2], j);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], sc[j], acc[i][j][v]);
+          }
+          if (i == RB) {
+            __builtin_amdgcn_sched_barrier(0);
+            wait_lgkm0();
+            wait_vm<OA::NLD>();
+            bar_nofence();
+            __builtin_amdgcn_sched_barrier(0);
+            get_scales(t + u + 2, u % 2);
+          }
+          if (i < RB) get_a(ra_[u % 3], i + RA);
+          else get_a(ra_[(u + 1) % 3], i - RB);
+          if (i >= RB) {
+            constexpr int NI = OA::NLD + OB::NLD;
+#pragma unroll
+            for (int p = (i - RB) * NI / RA; p < (i - RB + 1) * NI / RA; ++p) {
+              if (p < OB::NLD) issue_b(t + u + 2, rb_[u % 2], p);
+              else issue_a(t + u + 3, ra_[u % 3], p - OB::NLD);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-    } else {
+    }
+    wait_vm<0>();
+  } else {
+    // Half a stage is one k step of 32.  A row i of A's fragments meets all of
+    // B's in turn; as soon as its MFMAs are issued, its registers take row i of
+    // the next half, and B's two sets alternate, so that LDS reads run half a
+    // stage ahead of their use.  One barrier a stage, after the first row of
+    // the second half: then every wave holds the rest of stage t in registers
+    // (its buffers are free), and stage t + 1 has landed (all but the loads of
+    // A for stage t + 2).  The loads of a stage are spread over the rows.
+    u32x4 fa[FM], fb[2][FN];
+    auto get_a = [&](const char* op, int h, int i) {
+      fa[i] = AKC ? frag_kc(op + wm * (MT / WM) * 128, i, h) : frag_st(op, MT, wm * FM, i, h);
+    };
+    auto get_b = [&](const char* op, int h, int j) {
+      fb[h][j] = BKC ? frag_kc(op + wn * (NT / WN) * 128, j, h) : frag_st(op, NT, wn * FN, j, h);
+    };
+    auto row = [&](int h, int i) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 fa[FM], fb[FN];
+      for (int j = 0; j < FN; ++j) acc[i][j] = mfma_half<T>(fa[i], fb[h][j], acc[i][j]);
+    };
+    // what follows row i of a half: row i of A and a share of B for half h
+    // (B complete by the middle of the rows)
+    constexpr int BR = FM > 1 ? (FM + 1) / 2 : 1;
+    auto refill = [&](const char* ab, const char* bb, int h, int i) {
+      get_a(ab, h, i);
+      if (i < BR) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          fb[j] = BKC ? frag_kc(pb, j, h) : frag_st(pb, NT, wn * FN + j, h);
+        for (int j = i * FN / BR; j < (i + 1) * FN / BR; ++j) get_b(bb, h, j);
+      }
+    };
+    wait_vm<2 * OA::NLD + OB::NLD>();
+    bar_nofence();
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-          fa[i] = AKC ? frag_kc(pa, i, h) : frag_st(pa, MT, wm * FM + i, h);
+    for (int i = 0; i < FM; ++i) refill(ra_[0], rb_[0], 0, i);
+    for (int t = 0; t < nstage; t += 6) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+      for (int u = 0; u < 6; ++u) {
+        if (t + u >= nstage) break;
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = mfma_half<T>(fa[i], fb[j], acc[i][j]);
+        for (int i = 0; i < FM; ++i) {
+          row(0, i);
+          refill(ra_[u % 3], rb_[u % 2], 1, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          row(1, i);
+          if (i == 0) {
+            __builtin_amdgcn_sched_barrier(0);
+            wait_lgkm0();
+            wait_vm<OA::NLD>();
+            bar_nofence();
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          refill(ra_[(u + 1) % 3], rb_[(u + 1) % 2], 0, i);
+          constexpr int NI = OA::NLD + OB::NLD;
+#pragma unroll
+          for (int p = i * NI / FM; p < (i + 1) * NI / FM; ++p) {
+            if (p < OB::NLD) issue_b(t + u + 2, rb_[u % 2], p);
+            else issue_a(t + u + 3, ra_[u % 3], p - OB::NLD);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        want_rows(t + u + 4);
       }
     }
-  };
-
-  // ring: stage t + NBUF - 1 is requested as soon as every wave is done with
-  // the buffer it goes to (that of stage t - 1); whole rounds always run,
-  // stages past the end only wait and request nothing
-  want_rows(0);
-#pragma unroll
-  for (int b = 0; b < NBUF - 1; ++b) issue(b, ring[b]);
-  for (int t = 0; t < nstage; t += NBUF) {
-#pragma unroll
-    for (int u = 0; u < NBUF; ++u) {
-      wait_vm<(NBUF - 2) * (OA::NLD + OB::NLD)>();
-      wait_lgkm0();
-      bar_nofence();
-      issue(t + u + NBUF - 1, ring[(u + NBUF - 1) % NBUF]);
-      if (t + u < nstage) compute(ring[u], t + u);
-    }
+    wait_vm<0>();
   }
-  wait_vm<0>();
 
   // ---- outputs ----
+  // (every lane takes part in the exchange; rows and columns past the end
+  // write nothing)
+  static_assert(FM % 2 == 0, "fragments are stored in pairs");
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int n = n0 + wn * (NT / WN) + 16 * j + l16;
-    if (n - n0 >= nrow) continue;
     const size_t base = MODE == GROUP_DW ? ((size_t)g * a.d_out + n) * a.d_in : (size_t)(row0 + n) * a.ldo;
+    const bool have = n - n0 < nrow;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = m0 + wm * (MT / WM) + 16 * i + 4 * lg;
-      if (m < mdim) store4(a, base + m, acc[i][j], mdim - m);
+    for (int i = 0; i < FM; i += 2) {
+      const int m = m0 + wm * (MT / WM) + 16 * i + 8 * lg;
+      const int left = have ? mdim - m : 0;
+      if (a.out_dtype == 2) store8_32(a, base + m, acc[i][j], acc[i + 1][j], left);
+      else if (a.out_dtype == 1) store8_16<true>(a, base + m, acc[i][j], acc[i + 1][j], left);
+      else store8_16<false>(a, base + m, acc[i][j], acc[i + 1][j], left);
     }
   }
 }
@@ -489,7 +660,7 @@ long group_tile_grid(const GroupArgs& a, GroupMode mode, GroupTile t) {
   const long mtile = (mdim + mt - 1) / mt;
   long ntile;
   if (mode == GROUP_DW) {
-    ntile = (long)a.groups * ((a.d_out + nt - 1) / nt);
+    return (a.groups * mtile + 7) / 8 * 8 * ((a.d_out + nt - 1) / nt);
   } else if (a.groups == 1) {
     ntile = ((long)a.rows + nt - 1) / nt;
   } else {
@@ -502,21 +673,20 @@ long group_tile_grid(const GroupArgs& a, GroupMode mode, GroupTile t) {
 GroupTile choose_group_tile(const GroupArgs& a, GroupMode mode, GroupType) {
   const long avg = a.rows / a.groups;
   if (mode != GROUP_DW && avg <= 48) return TILE_128x32;
-  if (mode != GROUP_DW && avg < 512) return TILE_128x128;
   return group_tile_grid(a, mode, TILE_256x256) >= 256 ? TILE_256x256 : TILE_128x128;
 }
 
-template <typename T, int MODE, int MT, int NT, int WM, int WN, int NBUF>
+template <typename T, int MODE, int MT, int NT, int WM, int WN>
 static void go(const GroupArgs& a, long grid, hipStream_t s) {
-  hipLaunchKernelGGL((group_tile_kernel<T, MODE, MT, NT, WM, WN, NBUF>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((group_tile_kernel<T, MODE, MT, NT, WM, WN>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, s, a);
 }
 
 template <typename T, int MODE>
 static void go_tile(const GroupArgs& a, GroupTile t, long grid, hipStream_t s) {
-  if (t == TILE_256x256) go<T, MODE, 256, 256, 2, 4, 2>(a, grid, s);
-  else if (t == TILE_128x128 || MODE == GROUP_DW) go<T, MODE, 128, 128, 2, 2, 2>(a, grid, s);
-  else if constexpr (MODE != GROUP_DW) go<T, MODE, 128, 32, 4, 1, 3>(a, grid, s);
+  if (t == TILE_256x256) go<T, MODE, 256, 256, 2, 4>(a, grid, s);
+  else if (t == TILE_128x128 || MODE == GROUP_DW) go<T, MODE, 128, 128, 2, 2>(a, grid, s);
+  else if constexpr (MODE != GROUP_DW) go<T, MODE, 128, 32, 4, 1>(a, grid, s);
 }
 
 void launch_group_tile(const GroupArgs& a, GroupMode mode, GroupType type, GroupTile t, hipStream_t s) {

@@ -103,11 +103,11 @@ tq_status check_group(const tq_group_desc* d, bool e4m3, GroupMode mode, tq_dtyp
   return TQ_OK;
 }
 
-// the stride and alignment rule of four-value stores
+// the stride and alignment rule of 16-byte stores
 void set_out(GroupArgs* a, void* out, long ldo) {
   a->out = out;
   a->ldo = ldo;
-  a->vec_out = ldo % 4 == 0 && aligned(out, a->out_dtype == 2 ? 16 : 8) ? 1 : 0;
+  a->vec_out = ldo % (a->out_dtype == 2 ? 4 : 8) == 0 && aligned(out, 16) ? 1 : 0;
 }
 
 tq_status run_group(const GroupArgs& a, GroupMode mode, GroupType type, void* stream) {

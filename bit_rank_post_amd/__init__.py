@@ -166,7 +166,8 @@ _OPS = ("group_gemm", "group_gemm_dx", "group_gemm_dw", "fp8_gemm", "fp8_quant_r
 def __getattr__(name):
     if name in _OPS:
         from . import ops       # needs torch, which the rest of this module does not
-        return getattr(ops, name)
+        globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -26,7 +26,7 @@ SOURCES = [("route.hip", "route", []), ("colproj.hip", "colproj", []),
            ("gemm_decode.hip", "gemm_decode", []), ("decode_stages.hip", "decode_stages", []),
            ("combine.hip", "combine", []), ("upload.hip", "upload", []),
            ("router.hip", "router", []), ("pack.hip", "pack", []), ("calib.hip", "calib", []),
-           ("group_gemm.hip", "group_gemm", []), ("quant8.hip", "quant8", []), ("norm.hip", "norm", []),
+           ("group_gemm.hip", "group_gemm", []), ("group_rows.hip", "group_rows", []), ("quant8.hip", "quant8", []), ("norm.hip", "norm", []),
            ("tileq_host.cpp", "tileq_host", []), ("ops_host.cpp", "ops_host", [])]
 
 

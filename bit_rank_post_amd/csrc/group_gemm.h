@@ -32,6 +32,11 @@ struct GroupArgs {
   const float* ws;               // E4M3: [groups][ceil(d_out/128)][ceil(d_in/128)]
 };
 
+// Few rows per group (decode), Y only: 16 outputs x 16 rows per workgroup,
+// waves over k
+void launch_group_rows(const GroupArgs& a, GroupType type, hipStream_t s);
+long group_rows_grid(const GroupArgs& a);
+
 // Tile shapes of the LDS kernel (outputs x rows per workgroup).
 enum GroupTile { TILE_256x256 = 0, TILE_128x128 = 1, TILE_128x32 = 2 };
 

@@ -17,39 +17,54 @@ import ctypes
 import torch
 
 from . import (TQ_BF16, TQ_F16, TQ_F32, GroupDesc, NormDesc, NormGradDesc, Rows, TileQError, _check,
-               _ptr, lib)
+               lib)
 
 _DT = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16, torch.float32: TQ_F32}
 E4M3 = torch.float8_e4m3fn
 EINVAL, ESHAPE = 1, 2
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _refuse(fn, text, status=ESHAPE):
     raise TileQError("tq_" + fn, status, text)
 
 
-def _device(fn, **tensors):
-    """The one device of all tensors that are given."""
-    dev = None
-    for name, t in tensors.items():
+def _device(fn, *tensors):
+    """Index of the one device of all tensors that are given."""
+    dev = -1
+    for t in tensors:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-            _refuse(fn, f"{name} is not a tensor on a GPU", EINVAL)
-        if dev is not None and t.device != dev:
-            _refuse(fn, f"{name} is on {t.device}, not on {dev}", EINVAL)
-        dev = t.device
+        d = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if d < 0:
+            _refuse(fn, "an operand is not a tensor on a GPU", EINVAL)
+        if d != dev:
+            if dev >= 0:
+                _refuse(fn, f"operands on cuda:{dev} and cuda:{d}", EINVAL)
+            dev = d
     return dev
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream      # the handle alone, without a Stream object
 
 
 def _call(fn, dev, stream, *args):
     """Run the C entry with the tensors' device current, on `stream`."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-        name = "tq_" + fn
-        _check(name, getattr(lib(), name)(*args, ctypes.c_void_p(s)))
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    entry = getattr(lib(), "tq_" + fn)
+    if torch.cuda.current_device() == dev:
+        status = entry(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = entry(*args, stream)
+    if status:
+        _check("tq_" + fn, status)
 
 
 def _float(fn, t, name):
@@ -59,8 +74,8 @@ def _float(fn, t, name):
 
 
 def _shape(fn, t, name, *shape):
-    if tuple(t.shape) != tuple(shape):
-        _refuse(fn, f"{name} is {tuple(t.shape)}, must be {tuple(shape)}")
+    if t.shape != shape:
+        _refuse(fn, f"{name} is {tuple(t.shape)}, must be {shape}")
 
 
 def _dense(fn, t, name):
@@ -74,13 +89,14 @@ def _ld(fn, t, name):
     if t.dim() != 2:
         _refuse(fn, f"{name} must have two dimensions, not {t.dim()}")
     rows, d = t.shape
-    if d > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and d > 1:
         _refuse(fn, f"elements of a row of {name} must be neighbours")
     if rows <= 1:
         return d
-    if t.stride(0) < d:
+    if s0 < d:
         _refuse(fn, f"rows of {name} overlap")
-    return t.stride(0)
+    return s0
 
 
 def _int32(fn, t, name, n):
@@ -109,7 +125,7 @@ def group_gemm(x, w, y, off=None, src=None, src_div=1, stream=None):
     needed with one group), src int32 [rows] (without it row r of x).  w may
     also be one matrix [d_out][d_in]."""
     fn = "group_gemm"
-    dev = _device(fn, x=x, w=w, y=y, off=off, src=src)
+    dev = _device(fn, x, w, y, off, src)
     w = w[None] if w.dim() == 2 else w
     if w.dim() != 3:
         _refuse(fn, "w must be [groups][d_out][d_in]")
@@ -130,7 +146,7 @@ def group_gemm_dx(dy, w, dx, off=None, stream=None):
     grouped row: rows that were gathered from the same row of x are added by
     the caller (index_add_)."""
     fn = "group_gemm_dx"
-    dev = _device(fn, dy=dy, w=w, dx=dx, off=off)
+    dev = _device(fn, dy, w, dx, off)
     w = w[None] if w.dim() == 2 else w
     if w.dim() != 3:
         _refuse(fn, "w must be [groups][d_out][d_in]")
@@ -150,7 +166,7 @@ def group_gemm_dw(dy, x, dw, off=None, src=None, src_div=1, stream=None):
     (zero for an expert without rows): dy [rows][d_out] and x [x_rows][d_in]
     float16 or bfloat16, dw [groups][d_out][d_in] float16, bfloat16 or float32."""
     fn = "group_gemm_dw"
-    dev = _device(fn, dy=dy, x=x, dw=dw, off=off, src=src)
+    dev = _device(fn, dy, x, dw, off, src)
     dw = dw[None] if dw.dim() == 2 else dw
     if dw.dim() != 3:
         _refuse(fn, "dw must be [groups][d_out][d_in]")
@@ -173,7 +189,7 @@ def fp8_quant_rows(x, q, scale, stream=None):
     """x [rows][d] float16, bfloat16 or float32 -> q [rows][d] float8_e4m3fn with
     a scale for each 128 neighbours of a row, scale float32 [rows][ceil(d/128)]."""
     fn = "fp8_quant_rows"
-    dev = _device(fn, x=x, q=q, scale=scale)
+    dev = _device(fn, x, q, scale)
     xdt, ldx = _float(fn, x, "x"), _ld(fn, x, "x")
     rows, d = x.shape
     if q.dtype != E4M3 or scale.dtype != torch.float32:
@@ -190,7 +206,7 @@ def fp8_quant_blocks(w, q, scale, stream=None):
     of the same shape in float8_e4m3fn with a scale for each 128 x 128 block,
     scale float32 [groups][ceil(d_out/128)][ceil(d_in/128)]."""
     fn = "fp8_quant_blocks"
-    dev = _device(fn, w=w, q=q, scale=scale)
+    dev = _device(fn, w, q, scale)
     wdt = _float(fn, w, "w")
     if w.dim() not in (2, 3):
         _refuse(fn, "w must be [groups][d_out][d_in]")
@@ -209,7 +225,7 @@ def fp8_gemm(x, x_scale, w, w_scale, y, off=None, src=None, src_div=1, stream=No
     fp8_quant_blocks (w, w_scale): y [rows][d_out] float16, bfloat16 or
     float32.  src gathers the rows of x and of x_scale alike."""
     fn = "fp8_gemm"
-    dev = _device(fn, x=x, x_scale=x_scale, w=w, w_scale=w_scale, y=y, off=off, src=src)
+    dev = _device(fn, x, x_scale, w, w_scale, y, off, src)
     if w.dim() == 2:
         w, w_scale = w[None], w_scale[None]
     if w.dim() != 3:
@@ -231,22 +247,23 @@ def fp8_gemm(x, x_scale, w, w_scale, y, off=None, src=None, src_div=1, stream=No
 
 
 GATE_NONE, GATE_TOKEN, GATE_FULL = 0, 1, 2
+_ABSENT = Rows(None, 0)
 
 
 def _mat(fn, t, name, T, d, dtype):
     """tq_rows of an optional [T][d] tensor of one dtype."""
     if t is None:
-        return Rows(None, 0)
-    if t.dtype != dtype:
+        return _ABSENT
+    if t.dtype is not dtype:
         _refuse(fn, f"{name} is {t.dtype}, must be {dtype}", EINVAL)
-    ld = _ld(fn, t, name)
-    _shape(fn, t, name, T, d)
-    return Rows(t.data_ptr(), ld)
+    if t.shape != (T, d):
+        _refuse(fn, f"{name} is {tuple(t.shape)}, must be {(T, d)}")
+    return Rows(t.data_ptr(), _ld(fn, t, name))
 
 
 def _gate(fn, t, name, T, d, act):
     if t is None:
-        return GATE_NONE, Rows(None, 0)
+        return GATE_NONE, _ABSENT
     if t.dim() == 2:
         return GATE_FULL, _mat(fn, t, name, T, d, act)
     if t.dtype != torch.float32:
@@ -262,8 +279,10 @@ def _vec(fn, t, name, n, dtypes):
         return
     if t.dtype not in dtypes:
         _refuse(fn, f"{name} is {t.dtype}", EINVAL)
-    _shape(fn, t, name, n)
-    _dense(fn, t, name)
+    if t.shape != (n,):
+        _refuse(fn, f"{name} is {tuple(t.shape)}, must be {(n,)}")
+    if not t.is_contiguous():
+        _refuse(fn, f"{name} must be contiguous")
 
 
 def _weights(fn, w_post, w_next, d):
@@ -285,8 +304,8 @@ def norm_residual(x, y=None, n=None, b=None, w_post=None, w_next=None, gate=None
     rstd_post, rstd_next (float32 [T]) take 1 / rms for norm_residual_grad.
     y may be x, and n may be b."""
     fn = "norm_residual"
-    dev = _device(fn, x=x, y=y, n=n, b=b, w_post=w_post, w_next=w_next, gate=gate, rstd_post=rstd_post,
-                  rstd_next=rstd_next)
+    dev = _device(fn, x, y, n, b, w_post, w_next, gate, rstd_post,
+                  rstd_next)
     sdt, ldx = _float(fn, x, "x"), _ld(fn, x, "x")
     T, d = x.shape
     a = b if b is not None else n
@@ -313,9 +332,9 @@ def norm_residual_grad(y, dx=None, dy=None, dn=None, b=None, db=None, w_post=Non
     bytes for the weights' gradients (None: allocated by torch for the call).
     dx may be dy, and db may be dn."""
     fn = "norm_residual_grad"
-    dev = _device(fn, y=y, dx=dx, dy=dy, dn=dn, b=b, db=db, w_post=w_post, w_next=w_next, gate=gate,
-                  dgate=dgate, dw_post=dw_post, dw_next=dw_next, rstd_post=rstd_post, rstd_next=rstd_next,
-                  ws=ws)
+    dev = _device(fn, y, dx, dy, dn, b, db, w_post, w_next, gate,
+                  dgate, dw_post, dw_next, rstd_post, rstd_next,
+                  ws)
     sdt = _float(fn, y, "y")
     _ld(fn, y, "y")
     T, d = y.shape

@@ -16,8 +16,9 @@
 // same bits.
 //
 // Bound by memory: every input is read once and every output written once; a
-// row stays in the registers of its NTH threads (VPT vectors of 8 values
-// each) between the reductions.
+// row stays in the registers of its threads (VPT vectors of 8 values each)
+// between the reductions.  16384 x 4096 in bf16: forward 98 us, gradients 174
+// us, 5.5 and 4.6 TB/s of what they must move (a large copy: 5.0).
 #include "norm_ops.h"
 #include "tq_device.h"
 
@@ -52,6 +53,20 @@ __device__ __forceinline__ void store8<float>(float* p, const float v[8]) {
   *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
   *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
+// 8 neighbouring values as they lie in memory, for loads ahead of their use
+template <typename T> struct Raw8 {
+  typename Vec8<T>::type v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const typename Vec8<T>::type*>(p); }
+  __device__ __forceinline__ float get(int i) const { return (float)v[i]; }
+};
+template <> struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4*>(p);
+    b = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+};
 __device__ __forceinline__ void load8w(const void* p, int dt, int at, float v[8]) {
   if (dt == 0) load8(reinterpret_cast<const half_t*>(p) + at, v);
   else if (dt == 1) load8(reinterpret_cast<const __bf16*>(p) + at, v);
@@ -63,27 +78,28 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-// Sum over the NTH threads of a row (NTH = 64: each wave has a row of its
-// own).  s: NTH / 64 floats; a caller that reduces twice passes two arrays.
-template <int NTH>
+// Sum over the threads of a row: the workgroup, or with ROWS a wave (each wave
+// then has a row of its own).  s: 16 floats; a caller that reduces twice
+// passes two arrays.
+template <bool ROWS>
 __device__ __forceinline__ float row_sum(float v, float* s) {
   v = wave_sum(v);
-  if constexpr (NTH > 64) {
+  if constexpr (!ROWS) {
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
+    const int n = blockDim.x >> 6;
     v = 0.f;
-#pragma unroll
-    for (int i = 0; i < NTH / 64; ++i) v += s[i];
+    for (int i = 0; i < n; ++i) v += s[i];
   }
   return v;
 }
 
-template <typename S, typename A, int NTH, int VPT>
-__global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_forward_kernel(NormArgs a) {
-  constexpr int RPW = NTH == 64 ? 4 : 1;        // rows of a workgroup
-  __shared__ float s_a[NTH / 64], s_b[NTH / 64];
-  const long t = (long)blockIdx.x * RPW + (NTH == 64 ? threadIdx.x >> 6 : 0);
-  const int tid = NTH == 64 ? threadIdx.x & 63 : threadIdx.x;
+template <typename S, typename A, bool ROWS, int VPT>
+__global__ __launch_bounds__(ROWS ? 256 : 1024) void norm_forward_kernel(NormArgs a) {
+  __shared__ float s_a[16], s_b[16];
+  const int NTH = ROWS ? 64 : blockDim.x;       // threads of a row
+  const long t = ROWS ? (long)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int tid = ROWS ? threadIdx.x & 63 : threadIdx.x;
   if (t >= a.T) return;
   const int nv = a.d >> 3;
   float y[VPT][8], b[VPT][8];
@@ -106,7 +122,7 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_forward_kernel(Nor
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(b[i][j], b[i][j], ss);
-      r1 = rsqrtf(row_sum<NTH>(ss, s_a) / (float)a.d + a.eps);
+      r1 = rsqrtf(row_sum<ROWS>(ss, s_a) / (float)a.d + a.eps);
       if (a.rstd_post != nullptr && tid == 0) a.rstd_post[t] = r1;
     }
     const float k = a.gate == 1 ? a.alpha * reinterpret_cast<const float*>(a.gate_p)[t * a.ld_gate] : a.alpha;
@@ -131,7 +147,7 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_forward_kernel(Nor
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(y[i][j], y[i][j], ss);
-  const float r2 = rsqrtf(row_sum<NTH>(ss, s_b) / (float)a.d + a.eps);
+  const float r2 = rsqrtf(row_sum<ROWS>(ss, s_b) / (float)a.d + a.eps);
   if (a.rstd_next != nullptr && tid == 0) a.rstd_next[t] = r2;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -145,14 +161,16 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_forward_kernel(Nor
   }
 }
 
-// Workgroup w takes rows w, w + nparts, ...; (NTH = 64: each of its waves)
-template <typename S, typename A, int NTH, int VPT>
-__global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(NormArgs a) {
-  constexpr int RPW = NTH == 64 ? 4 : 1;
-  __shared__ float s_a[2][NTH / 64], s_b[2][NTH / 64];
-  const int part = blockIdx.x * RPW + (NTH == 64 ? threadIdx.x >> 6 : 0);
-  const int tid = NTH == 64 ? threadIdx.x & 63 : threadIdx.x;
-  if (part >= a.nparts) return;
+// Workgroup w takes rows w, w + nparts, ... (with ROWS: its waves rows 4w .. 4w+3,
+// then 4 nparts further on)
+template <typename S, typename A, bool ROWS, int VPT>
+__global__ __launch_bounds__(ROWS ? 256 : 1024) void norm_backward_kernel(NormArgs a) {
+  __shared__ float s_a[2][16], s_b[2][16];
+  const int NTH = ROWS ? 64 : blockDim.x;
+  const int part = blockIdx.x;
+  const int tid = ROWS ? threadIdx.x & 63 : threadIdx.x;
+  const long first = ROWS ? (long)part * 4 + (threadIdx.x >> 6) : part;
+  const long stride = ROWS ? (long)a.nparts * 4 : a.nparts;
   const int nv = a.d >> 3;
   const float inv_d = 1.f / (float)a.d;
   const bool has_b = a.b != nullptr, has_post = a.w_post != nullptr, has_next = a.dn != nullptr;
@@ -161,17 +179,44 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(No
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) gp[i][j] = gn[i][j] = 0.f;
+  // With one vector a thread, a row's inputs are requested while the row before
+  // it is worked on (two vectors do not fit 128 registers so).
+  constexpr bool AHEAD = VPT == 1;
+  Raw8<S> q_dy[VPT], q_y[VPT];
+  Raw8<A> q_dn[VPT], q_b[VPT];
+  auto request = [&](long t) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = tid + i * NTH;
+      if (c >= nv) continue;
+      if (a.dy != nullptr) q_dy[i].load(reinterpret_cast<const S*>(a.dy) + t * a.ld_dy + c * 8);
+      if (has_next) {
+        q_y[i].load(reinterpret_cast<const S*>(a.y) + t * a.ld_y + c * 8);
+        q_dn[i].load(reinterpret_cast<const A*>(a.dn) + t * a.ld_dn + c * 8);
+      }
+      if (has_b) q_b[i].load(reinterpret_cast<const A*>(a.b) + t * a.ld_b + c * 8);
+    }
+  };
   int ph = 0;
-  for (long t = part; t < a.T; t += a.nparts, ph ^= 1) {
+  if (AHEAD && first < a.T) request(first);
+  for (long t = first; t < a.T; t += stride, ph ^= 1) {
+    if (!AHEAD) request(t);
     float u[VPT][8], dx[VPT][8];
-    // dx
+    Raw8<S> y_[VPT];
+    Raw8<A> dn_[VPT], b_[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = tid + i * NTH;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = dx[i][j] = 0.f;
-      if (c < nv && a.dy != nullptr) load8(reinterpret_cast<const S*>(a.dy) + t * a.ld_dy + c * 8, dx[i]);
+      for (int j = 0; j < 8; ++j) {
+        u[i][j] = 0.f;
+        dx[i][j] = c < nv && a.dy != nullptr ? q_dy[i].get(j) : 0.f;
+      }
+      y_[i] = q_y[i];
+      dn_[i] = q_dn[i];
+      b_[i] = q_b[i];
     }
+    if (AHEAD && t + stride < a.T) request(t + stride);
     if (has_next) {
       const float r2 = a.rstd_next[t];
       float h[VPT][8];
@@ -183,18 +228,17 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(No
         for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
         if (c >= nv) continue;
         float w[8];
-        load8(reinterpret_cast<const S*>(a.y) + t * a.ld_y + c * 8, u[i]);
-        load8(reinterpret_cast<const A*>(a.dn) + t * a.ld_dn + c * 8, h[i]);
         load8w(a.w_next, a.wdt, c * 8, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          u[i][j] *= r2;
+          u[i][j] = y_[i].get(j) * r2;
+          h[i][j] = dn_[i].get(j);
           gn[i][j] = __builtin_fmaf(h[i][j], u[i][j], gn[i][j]);
           h[i][j] *= w[j];
           dot = __builtin_fmaf(h[i][j], u[i][j], dot);
         }
       }
-      const float mean = row_sum<NTH>(dot, s_a[ph]) * inv_d;
+      const float mean = row_sum<ROWS>(dot, s_a[ph]) * inv_d;
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -219,7 +263,8 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(No
       float w[8], g[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = g[j] = 1.f;
-      load8(reinterpret_cast<const A*>(a.b) + t * a.ld_b + c * 8, u[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[i][j] = b_[i].get(j);
       if (has_post) load8w(a.w_post, a.wdt, c * 8, w);
       if (a.gate == 2) {
         load8(reinterpret_cast<const A*>(a.gate_p) + t * a.ld_gate + c * 8, g);
@@ -240,7 +285,7 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(No
       }
     }
     float sum = 0.f;
-    if (has_post || a.gate == 1) sum = row_sum<NTH>(dot, s_b[ph]);
+    if (has_post || a.gate == 1) sum = row_sum<ROWS>(dot, s_b[ph]);
     if (a.gate == 1 && a.dgate != nullptr && tid == 0)
       reinterpret_cast<float*>(a.dgate)[t * a.ld_dgate] = sum;
     if (a.db == nullptr) continue;
@@ -255,6 +300,27 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(No
       store8(reinterpret_cast<A*>(a.db) + t * a.ld_db + c * 8, o);
     }
   }
+  if constexpr (ROWS) {
+    // the four waves' sums first, in wave order
+    __shared__ float s_w[3][2][8][64];
+    const int wave = threadIdx.x >> 6;
+    if (wave > 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s_w[wave - 1][0][j][tid] = gp[0][j];
+        s_w[wave - 1][1][j][tid] = gn[0][j];
+      }
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        gp[0][j] += s_w[w][0][j][tid];
+        gn[0][j] += s_w[w][1][j][tid];
+      }
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * NTH;
@@ -265,65 +331,69 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void norm_backward_kernel(No
 }
 
 // dw[c] = sum over the parts, in a fixed order: 32 columns a workgroup, the
-// parts in 8 interleaved runs, joined in LDS
-__global__ __launch_bounds__(256) void norm_join_kernel(NormArgs a) {
-  __shared__ float s[8][33];
+// parts in 32 interleaved runs of four sums each, joined in LDS
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float* dw = blockIdx.y == 0 ? a.dw_post : a.dw_next;
   if (dw == nullptr) return;
   const float* p = a.part + (blockIdx.y == 0 ? 0 : (size_t)a.nparts * a.d);
-  float v = 0.f;
-  if (c < a.d)
-    for (int i = run; i < a.nparts; i += 8) v += p[(size_t)i * a.d + c];
-  s[run][lane] = v;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < a.d) {
+    for (int i = run; i < a.nparts; i += 128) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + 32 * k < a.nparts) v[k] += p[(size_t)(i + 32 * k) * a.d + c];
+    }
+  }
+  s[run][lane] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
   if (run == 0 && c < a.d) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[i][lane];
+    for (int i = 0; i < 32; ++i) t += s[i][lane];
     dw[c] = t;
   }
 }
 
-// Threads per row and vectors per thread: one wave and up to 4 vectors for
-// rows up to 2048, 256 threads and up to 4 for rows up to 8192, 1024 threads
-// and 2 above.
+// Threads of a row of nv vectors with vpt a thread, in whole waves (5632
+// values: 704 threads, all at work, or 352 with two vectors).
+static int row_threads(int nv, int vpt) { return ((nv + vpt - 1) / vpt + 63) / 64 * 64; }
+
+// Rows up to 512 values are a wave's, longer ones a workgroup's with two
+// vectors a thread (16384 x 4096 in bf16: 98 us; one vector 98, four 111; at
+// 5632: 106, 114, 117).
 template <typename S, typename A>
 static void forward_go(const NormArgs& a, hipStream_t s) {
   const int nv = a.d >> 3;
-  const dim3 rows((unsigned)a.T), rows4((unsigned)((a.T + 3) / 4));
-#define GO(NTH, VPT) hipLaunchKernelGGL((norm_forward_kernel<S, A, NTH, VPT>), NTH == 64 ? rows4 : rows, \
-                                        dim3(NTH == 64 ? 256 : NTH), 0, s, a)
-  if (nv <= 64) GO(64, 1);
-  else if (nv <= 256) GO(256, 1);
-  else if (nv <= 512) GO(256, 2);
-  else if (nv <= 1024) GO(256, 4);
-  else GO(1024, 2);
-#undef GO
+  if (nv <= 64)
+    hipLaunchKernelGGL((norm_forward_kernel<S, A, true, 1>), dim3((a.T + 3) / 4), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_forward_kernel<S, A, false, 2>), dim3(a.T), dim3(row_threads(nv, 2)), 0, s, a);
 }
 
-// Rows are dealt to this many workgroups (or waves): two workgroups of 256
-// threads for each of the 256 CUs, or as many waves.
+// Rows are dealt to as many workgroups as run at once, 1024 threads on each of
+// 256 CUs: more only add partial sums (16384 x 4096 in bf16: 256
+// workgroups of 512 threads 202 us, 512 166 us, 1024 179 us).
 int norm_parts(int T, int d) {
-  const int most = (d >> 3) <= 64 ? 2048 : 512;
-  return T < most ? (T > 0 ? T : 1) : most;
+  const int nv = d >> 3;
+  const int most = nv <= 64 ? 1024 : 256 * (1024 / row_threads(nv, nv <= 1024 ? 1 : 2));
+  const int want = nv <= 64 ? (T + 3) / 4 : T;
+  return want < most ? (want > 0 ? want : 1) : most;
 }
 
 template <typename S, typename A>
 static void backward_go(const NormArgs& a, hipStream_t s) {
   const int nv = a.d >> 3;
-  const dim3 g((unsigned)a.nparts), g4((unsigned)((a.nparts + 3) / 4));
-#define GO(NTH, VPT) hipLaunchKernelGGL((norm_backward_kernel<S, A, NTH, VPT>), NTH == 64 ? g4 : g, \
-                                        dim3(NTH == 64 ? 256 : NTH), 0, s, a)
-  if (nv <= 64) GO(64, 1);
-  else if (nv <= 256) GO(256, 1);
-  else if (nv <= 512) GO(256, 2);
-  else if (nv <= 1024) GO(512, 2);
-  else GO(1024, 2);
-#undef GO
+  if (nv <= 64)
+    hipLaunchKernelGGL((norm_backward_kernel<S, A, true, 1>), dim3(a.nparts), dim3(256), 0, s, a);
+  else if (nv <= 1024)
+    hipLaunchKernelGGL((norm_backward_kernel<S, A, false, 1>), dim3(a.nparts), dim3(row_threads(nv, 1)), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_backward_kernel<S, A, false, 2>), dim3(a.nparts), dim3(row_threads(nv, 2)), 0, s, a);
   if (a.dw_post != nullptr || a.dw_next != nullptr)
-    hipLaunchKernelGGL(norm_join_kernel, dim3((a.d + 31) / 32, 2), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(norm_join_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, s, a);
 }
 
 template <bool FWD, typename S>

@@ -28,7 +28,8 @@ EXPORTS = ["tq_layer_create", "tq_upload_proj", "tq_upload_shared_expert",
            "tq_profile_enable", "tq_profile_read", "tq_pack_workspace_size", "tq_pack_proj",
            "tq_calibrate_read", "tq_group_gemm", "tq_group_gemm_dx", "tq_group_gemm_dw", "tq_fp8_gemm",
            "tq_fp8_quant_rows", "tq_fp8_quant_blocks", "tq_norm_residual", "tq_norm_grad_workspace_size",
-           "tq_norm_residual_grad"]
+           "tq_norm_residual_grad", "tq_group_slots_workspace_size", "tq_group_slots",
+           "tq_block_workspace_size", "tq_block_forward"]
 STAGES = ["route", "row_exponent", "column_stage_in", "gemm_in", "column_stage_down",
           "shared_expert", "gemm_down", "combine"]
 
@@ -91,6 +92,12 @@ class NormGradDesc(ctypes.Structure):
                                                   "dw_post", "dw_next")])
 
 
+class BlockDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("topk", "stream_dtype", "w_dtype", "gate")]
+                + [("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("w_pre", "w_post", "router")] + [("gate_v", Rows)])
+
+
 _lib = None
 
 
@@ -133,6 +140,10 @@ def lib():
         L.tq_norm_residual.argtypes = [ctypes.POINTER(NormDesc), vp]
         L.tq_norm_grad_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
         L.tq_norm_residual_grad.argtypes = [ctypes.POINTER(NormGradDesc), vp, sz, vp]
+        L.tq_group_slots_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        L.tq_group_slots.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.tq_block_workspace_size.argtypes = [vp, i32, i32, ctypes.POINTER(sz)]
+        L.tq_block_forward.argtypes = [vp, ctypes.POINTER(BlockDesc), vp, i32, vp, vp, vp, vp, sz, vp]
         for name in EXPORTS:
             if name not in ("tq_last_error", "tq_abi_version"):
                 getattr(L, name).restype = i32
@@ -160,7 +171,8 @@ def _stream(stream):
 
 # The operators around a layer (defined in ops.py, offered here)
 _OPS = ("group_gemm", "group_gemm_dx", "group_gemm_dw", "fp8_gemm", "fp8_quant_rows",
-        "fp8_quant_blocks", "norm_residual", "norm_residual_grad")
+        "fp8_quant_blocks", "norm_residual", "norm_residual_grad",
+        "group_slots", "group_slots_workspace")
 
 
 def __getattr__(name):
@@ -262,6 +274,19 @@ class Layer:
         """tq_forward on the library's static scratch array (no workspace)."""
         _check("tq_forward_noalloc", lib().tq_forward_noalloc(
             self.h, _ptr(x), T, _ptr(ids), _ptr(gates), topk, _ptr(y), y_dtype, _stream(stream)))
+
+    def block_workspace_size(self, T: int, topk: int) -> int:
+        n = ctypes.c_size_t()
+        _check("tq_block_workspace_size", lib().tq_block_workspace_size(self.h, T, topk, ctypes.byref(n)))
+        return n.value
+
+    def block_forward(self, x, y, router, w_pre, topk, ids_out, gates_out, ws, w_post=None, gate=None,
+                      alpha=1.0, eps=1e-6, stream=None):
+        """A whole block on the residual stream x [T][d_model]: pre-norm, router,
+        this layer, post-norm, gate and residual into y (which may be x).  The
+        routing lands in ids_out / gates_out."""
+        from .ops import block_forward
+        block_forward(self, x, y, router, w_pre, topk, ids_out, gates_out, ws, w_post, gate, alpha, eps, stream)
 
     def debug_route(self, which, ids, T, topk, ws, cnt, off, perm, inv, col_off, col_tok,
                     slot2col, stream=None):

@@ -168,7 +168,39 @@ tq_status check_vec(const void* p, const char* name) {
   return TQ_OK;
 }
 
+tq_status check_norm_forward(const tq_norm_desc* d, NormArgs* a) {
+  if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
+  TRY(check_norm(d->T, d->d, d->stream_dtype, d->act, d->w_dtype, d->gate, d->alpha));
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return fail(TQ_EINVAL, "eps must be finite and >= 0");
+  const bool has_b = d->b.p != nullptr, has_n = d->n.p != nullptr;
+  if (has_b != (d->y.p != nullptr))
+    return fail(TQ_EINVAL, "b and y go together (y = x + alpha gate p(b))");
+  if (!has_b && !has_n && d->T > 0) return fail(TQ_EINVAL, "neither y nor n is asked for");
+  if (!has_b && (d->w_post || d->gate != TQ_GATE_NONE)) return fail(TQ_EINVAL, "w_post and gate need b");
+  if (has_n && !d->w_next) return fail(TQ_EINVAL, "w_next is NULL");
+  if (d->rstd_post && !d->w_post) return fail(TQ_EINVAL, "rstd_post needs w_post");
+  if (d->rstd_next && !has_n) return fail(TQ_EINVAL, "rstd_next needs n");
+  TRY(check_rows(d->x, "x", d->T > 0, d->d, d->stream_dtype, &a->ld_x));
+  TRY(check_rows(d->y, "y", false, d->d, d->stream_dtype, &a->ld_y));
+  TRY(check_rows(d->b, "b", false, d->d, d->act, &a->ld_b));
+  TRY(check_rows(d->n, "n", false, d->d, d->act, &a->ld_n));
+  TRY(check_gate(d->gate_v, "gate", d->gate, d->d, d->act, d->T > 0, &a->ld_gate));
+  TRY(check_vec(d->w_post, "w_post"));
+  TRY(check_vec(d->w_next, "w_next"));
+  if (!aligned(d->rstd_post, 4) || !aligned(d->rstd_next, 4)) return fail(TQ_EINVAL, "rstd not 4-byte aligned");
+  // one workgroup of up to 1024 threads a row
+  if (d->T > 0x3FFFFF) return fail(TQ_EUNSUPPORTED, "T = %d >= 2^22", d->T);
+  return TQ_OK;
+}
+
 }  // namespace
+
+namespace tq {
+tq_status check_norm_residual(const tq_norm_desc* d) {
+  NormArgs a{};
+  return check_norm_forward(d, &a);
+}
+}  // namespace tq
 
 extern "C" {
 
@@ -258,28 +290,8 @@ tq_status tq_fp8_quant_blocks(const void* w, tq_dtype w_dtype, int32_t groups, i
 }
 
 tq_status tq_norm_residual(const tq_norm_desc* d, void* stream) {
-  if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
-  TRY(check_norm(d->T, d->d, d->stream_dtype, d->act, d->w_dtype, d->gate, d->alpha));
-  if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return fail(TQ_EINVAL, "eps must be finite and >= 0");
-  const bool has_b = d->b.p != nullptr, has_n = d->n.p != nullptr;
-  if (has_b != (d->y.p != nullptr))
-    return fail(TQ_EINVAL, "b and y go together (y = x + alpha gate p(b))");
-  if (!has_b && !has_n && d->T > 0) return fail(TQ_EINVAL, "neither y nor n is asked for");
-  if (!has_b && (d->w_post || d->gate != TQ_GATE_NONE)) return fail(TQ_EINVAL, "w_post and gate need b");
-  if (has_n && !d->w_next) return fail(TQ_EINVAL, "w_next is NULL");
-  if (d->rstd_post && !d->w_post) return fail(TQ_EINVAL, "rstd_post needs w_post");
-  if (d->rstd_next && !has_n) return fail(TQ_EINVAL, "rstd_next needs n");
   NormArgs a{};
-  TRY(check_rows(d->x, "x", d->T > 0, d->d, d->stream_dtype, &a.ld_x));
-  TRY(check_rows(d->y, "y", false, d->d, d->stream_dtype, &a.ld_y));
-  TRY(check_rows(d->b, "b", false, d->d, d->act, &a.ld_b));
-  TRY(check_rows(d->n, "n", false, d->d, d->act, &a.ld_n));
-  TRY(check_gate(d->gate_v, "gate", d->gate, d->d, d->act, d->T > 0, &a.ld_gate));
-  TRY(check_vec(d->w_post, "w_post"));
-  TRY(check_vec(d->w_next, "w_next"));
-  if (!aligned(d->rstd_post, 4) || !aligned(d->rstd_next, 4)) return fail(TQ_EINVAL, "rstd not 4-byte aligned");
-  // one workgroup of up to 1024 threads a row
-  if (d->T > 0x3FFFFF) return fail(TQ_EUNSUPPORTED, "T = %d >= 2^22", d->T);
+  TRY(check_norm_forward(d, &a));
   if (d->T == 0) return TQ_OK;
   a.T = d->T;
   a.d = d->d;

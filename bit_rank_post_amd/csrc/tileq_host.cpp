@@ -81,6 +81,7 @@ struct tq_layer {
 };
 
 namespace tq {
+tq_status check_norm_residual(const tq_norm_desc* d);      // ops_host.cpp
 void set_last_error(const char* text) { g_err = text; }
 
 // Compute units of the current device (cached per device id; concurrent
@@ -1204,6 +1205,161 @@ tq_status tq_layer_destroy(tq_layer* L) {
   if (L->fork_ev) (void)hipEventDestroy(L->fork_ev);
   if (L->join_ev) (void)hipEventDestroy(L->join_ev);
   delete L;
+  return TQ_OK;
+}
+
+}  // extern "C"
+
+// ---- the block around a layer ------------------------------------------------
+
+namespace {
+struct BlockPlan {
+  size_t n, logits, b, fwd, total;
+};
+BlockPlan block_plan(const tq_layer* L, int T, size_t fwd_bytes) {
+  BlockPlan p{};
+  size_t o = align256(fwd_bytes);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align256(o + bytes);
+    return at;
+  };
+  p.fwd = 0;
+  p.n = take((size_t)T * L->d_model * 2);
+  p.logits = take((size_t)T * L->K * sizeof(float));
+  p.b = take((size_t)T * L->d_model * 2);
+  p.total = o;
+  return p;
+}
+}  // namespace
+
+extern "C" {
+
+tq_status tq_block_workspace_size(const tq_layer* L, int32_t T, int32_t topk, size_t* bytes) {
+  size_t fwd = 0;
+  if (!bytes) return fail(TQ_EINVAL, "bytes is NULL");
+  const tq_status st = tq_workspace_size(L, T, topk, &fwd);
+  if (st != TQ_OK) return st;
+  *bytes = block_plan(L, T, fwd).total;
+  return TQ_OK;
+}
+
+tq_status tq_block_forward(const tq_layer* L, const tq_block_desc* d, const void* x, int32_t T,
+                           int32_t* topk_ids, float* topk_w, void* y, void* ws, size_t ws_bytes,
+                           void* stream) {
+  tq_status st = check_ready(L);
+  if (st != TQ_OK) return st;
+  if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
+  if (L->kind != TQ_SWIGLU) return fail(TQ_EINVAL, "a block needs a SWIGLU layer (its output is the stream's width)");
+  if (d->topk < 1 || d->topk > std::min(L->K, 32))
+    return fail(TQ_ESHAPE, "topk = %d outside [1, min(K, 32)]", d->topk);
+  st = check_tokens(T, d->topk);
+  if (st != TQ_OK) return st;
+  size_t fwd = 0;
+  st = tq_workspace_size(L, T, d->topk, &fwd);
+  if (st != TQ_OK) return st;
+  if (T == 0) return TQ_OK;
+  const BlockPlan p = block_plan(L, T, fwd);
+  // every argument of the four steps is checked before the first is launched
+  tq_norm_desc pre{}, post{};
+  pre.T = post.T = T;
+  pre.d = post.d = L->d_model;
+  pre.stream_dtype = post.stream_dtype = d->stream_dtype;
+  pre.act = post.act = L->act;
+  pre.w_dtype = post.w_dtype = d->w_dtype;
+  pre.eps = post.eps = d->eps;
+  pre.alpha = 1.f;
+  post.alpha = d->alpha;
+  if (!x || !y || !ws || !topk_ids || !topk_w) return fail(TQ_EINVAL, "NULL buffer");
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return fail(TQ_EINVAL, "ws not 256-byte aligned");
+  if (ws_bytes < p.total) return fail(TQ_ESHAPE, "ws_bytes = %zu < %zu", ws_bytes, p.total);
+  if (!d->router) return fail(TQ_EINVAL, "router is NULL");
+  if (reinterpret_cast<uintptr_t>(d->router) & 15) return fail(TQ_EINVAL, "router not 16-byte aligned");
+  if ((long)T * L->d_model * 2 >= 0x7FFFFFF0L)
+    return fail(TQ_EUNSUPPORTED, "T * d_model * 2 = %ld bytes of activations >= 2^31", (long)T * L->d_model * 2);
+  pre.x.p = const_cast<void*>(x);
+  pre.n.p = at<void>(ws, p.n);
+  pre.w_next = d->w_pre;
+  post.x.p = const_cast<void*>(x);
+  post.b.p = at<void>(ws, p.b);
+  post.y.p = y;
+  post.w_post = d->w_post;
+  post.gate = d->gate;
+  post.gate_v = d->gate_v;
+  st = check_norm_residual(&pre);
+  if (st != TQ_OK) return st;
+  st = check_norm_residual(&post);
+  if (st != TQ_OK) return st;
+  st = tq_norm_residual(&pre, stream);
+  if (st != TQ_OK) return st;
+  tq_group_desc g{};
+  g.groups = 1;
+  g.rows = T;
+  g.d_in = L->d_model;
+  g.d_out = L->K;
+  g.act = L->act;
+  st = tq_group_gemm(&g, at<void>(ws, p.n), d->router, at<float>(ws, p.logits), TQ_F32, stream);
+  if (st != TQ_OK) return st;
+  st = tq_forward_from_logits(L, at<void>(ws, p.n), T, at<float>(ws, p.logits), d->topk, topk_ids, topk_w,
+                              at<void>(ws, p.b), L->act, ws, fwd, stream);
+  if (st != TQ_OK) return st;
+  return tq_norm_residual(&post, stream);
+}
+
+// ---- grouping without a layer ------------------------------------------------
+
+tq_status tq_group_slots_workspace_size(int32_t T, int32_t topk, int32_t K, size_t* bytes) {
+  if (!bytes) return fail(TQ_EINVAL, "bytes is NULL");
+  const tq_status st = check_tokens(T, topk);
+  if (st != TQ_OK) return st;
+  if (K < 1 || K > 256) return fail(TQ_ESHAPE, "K = %d outside [1, 256]", K);
+  const size_t S = (size_t)T * topk, nb = (S + 1023) / 1024 + 1;
+  size_t o = 256;                                        // flags
+  for (size_t n : {(size_t)K, (size_t)K + 1, (size_t)K + 1, S, (S + 63) / 64 * K, (size_t)2 * T + 1, 64 * nb, nb,
+                   (size_t)1})
+    o = align256(o + sizeof(int) * n);
+  *bytes = o;
+  return TQ_OK;
+}
+
+tq_status tq_group_slots(const int32_t* topk_ids, int32_t T, int32_t topk, int32_t K, int32_t* off,
+                         int32_t* perm, int32_t* inv, void* ws, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  const tq_status st = tq_group_slots_workspace_size(T, topk, K, &need);
+  if (st != TQ_OK) return st;
+  if (T == 0) return TQ_OK;
+  if (!topk_ids || !off || !perm || !inv || !ws) return fail(TQ_EINVAL, "NULL buffer");
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return fail(TQ_EINVAL, "ws not 256-byte aligned");
+  if (ws_bytes < need) return fail(TQ_ESHAPE, "ws_bytes = %zu < %zu", ws_bytes, need);
+  const size_t S = (size_t)T * topk, nb = (S + 1023) / 1024 + 1;
+  RouteArgs r{};
+  r.ids = topk_ids;
+  r.T = T;
+  r.k = topk;
+  r.S = (int)S;
+  r.K = K;
+  r.bm_gemm = r.rt_col = 128;
+  r.off = off;
+  r.perm = perm;
+  r.inv = inv;
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    int* p = at<int>(ws, o);
+    o = align256(o + sizeof(int) * n);
+    return p;
+  };
+  r.flags = take(64);
+  r.cnt = take(K);
+  r.tile_gemm = take(K + 1);
+  r.tile_colx = take(K + 1);
+  r.rank = take(S);
+  r.cntw = take((S + 63) / 64 * K);
+  r.colmask = take((size_t)2 * T + 1);
+  r.wgcnt = take(64 * nb);
+  r.dropw = take(nb);
+  r.zero_init = reinterpret_cast<unsigned*>(take(1));
+  launch_route(r, reinterpret_cast<hipStream_t>(stream));
+  HIPCHK(hipGetLastError());
   return TQ_OK;
 }
 

@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import (TQ_BF16, TQ_F16, TQ_F32, GroupDesc, NormDesc, NormGradDesc, Rows, TileQError, _check,
+from . import (TQ_BF16, TQ_F16, TQ_F32, BlockDesc, GroupDesc, NormDesc, NormGradDesc, Rows, TileQError, _check,
                lib)
 
 _DT = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16, torch.float32: TQ_F32}
@@ -99,12 +99,12 @@ def _ld(fn, t, name):
     return s0
 
 
-def _int32(fn, t, name, n):
+def _int32(fn, t, name, *shape):
     if t is None:
         return
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         _refuse(fn, f"{name} is {t.dtype}, must be int32", EINVAL)
-    _shape(fn, t, name, n)
+    _shape(fn, t, name, *shape)
     _dense(fn, t, name)
 
 
@@ -372,3 +372,61 @@ def norm_grad_workspace(T, d):
     n = ctypes.c_size_t()
     _check("tq_norm_grad_workspace_size", lib().tq_norm_grad_workspace_size(T, d, ctypes.byref(n)))
     return n.value
+
+
+def group_slots_workspace(T, topk, K):
+    """Bytes of workspace of group_slots."""
+    n = ctypes.c_size_t()
+    _check("tq_group_slots_workspace_size", lib().tq_group_slots_workspace_size(T, topk, K, ctypes.byref(n)))
+    return n.value
+
+
+def group_slots(ids, K, off, perm, inv, ws, stream=None):
+    """Slots of router ids (int32 [T][topk]) grouped by expert: off int32
+    [K + 1], perm int32 [T * topk] (the src of the grouped products, with
+    src_div = topk), inv int32 [T * topk] (row of each slot, -1 for an id
+    outside [0, K)).  ws: uint8 tensor of group_slots_workspace(T, topk, K)
+    bytes; its first int32 holds the number of dropped slots afterwards."""
+    fn = "group_slots"
+    dev = _device(fn, ids, off, perm, inv, ws)
+    if ids.dim() != 2:
+        _refuse(fn, "ids must be [T][topk]")
+    T, k = ids.shape
+    _int32(fn, ids, "ids", T, k)
+    _int32(fn, off, "off", K + 1)
+    _int32(fn, perm, "perm", T * k)
+    _int32(fn, inv, "inv", T * k)
+    _dense(fn, ws, "ws")
+    _call(fn, dev, stream, _ptr(ids), T, k, K, _ptr(off), _ptr(perm), _ptr(inv), _ptr(ws),
+          ws.numel() * ws.element_size())
+
+
+def block_forward(layer, x, y, router, w_pre, topk, ids_out, gates_out, ws, w_post=None, gate=None, alpha=1.0,
+                  eps=1e-6, stream=None):
+    """Layer.block_forward."""
+    fn = "block_forward"
+    dev = _device(fn, x, y, router, w_pre, ids_out, gates_out, ws, w_post, gate)
+    act = torch.float16 if layer.act == TQ_F16 else torch.bfloat16
+    sdt, T, d = _float(fn, x, "x"), x.shape[0], layer.d_model
+    for name, t in (("x", x), ("y", y)):
+        _shape(fn, t, name, T, d)
+        _dense(fn, t, name)
+        if t.dtype is not x.dtype:
+            _refuse(fn, f"{name} is {t.dtype}, must be {x.dtype}", EINVAL)
+    _shape(fn, router, "router", layer.K, d)
+    _dense(fn, router, "router")
+    if router.dtype is not act:
+        _refuse(fn, f"router is {router.dtype}, must be {act}", EINVAL)
+    if w_pre is None:
+        _refuse(fn, "w_pre is needed", EINVAL)
+    _int32(fn, ids_out, "ids_out", T, topk)
+    _shape(fn, gates_out, "gates_out", T, topk)
+    _dense(fn, gates_out, "gates_out")
+    _dense(fn, ws, "ws")
+    if gates_out.dtype is not torch.float32:
+        _refuse(fn, f"gates_out is {gates_out.dtype}, must be float32", EINVAL)
+    kind, g = _gate(fn, gate, "gate", T, d, act)
+    desc = BlockDesc(topk, sdt, _weights(fn, w_post, w_pre, d), kind, alpha, eps, _ptr(w_pre), _ptr(w_post),
+                     _ptr(router), g)
+    _call(fn, dev, stream, layer.h, ctypes.byref(desc), _ptr(x), T, _ptr(ids_out), _ptr(gates_out), _ptr(y),
+          _ptr(ws), ws.numel() * ws.element_size())

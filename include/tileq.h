@@ -411,6 +411,46 @@ typedef struct {
 tq_status tq_norm_grad_workspace_size(int32_t T, int32_t d, size_t *bytes);
 tq_status tq_norm_residual_grad(const tq_norm_grad_desc *d, void *ws, size_t ws_bytes, void *stream);
 
+/* The slots t*topk+j of router ids (DEVICE int32 [T][topk]; tq_router_topk)
+ * grouped by expert, for tq_group_desc: off DEVICE int32 [K+1], perm DEVICE
+ * int32 [T*topk] (the slots in (expert, slot) order: src with src_div = topk;
+ * entries past off[K] unspecified), inv DEVICE int32 [T*topk] (row of each
+ * slot, -1 for an id outside [0, K), which is dropped).  ws: DEVICE, 256-byte
+ * aligned, tq_group_slots_workspace_size() bytes; ((int32_t*)ws)[0] holds the
+ * number of dropped slots afterwards.  K <= 256; T = 0 writes nothing.
+ * Errors: TQ_EINVAL, TQ_ESHAPE, TQ_EHIP. */
+tq_status tq_group_slots_workspace_size(int32_t T, int32_t topk, int32_t K, size_t *bytes);
+tq_status tq_group_slots(const int32_t *topk_ids, int32_t T, int32_t topk, int32_t K, int32_t *off,
+                         int32_t *perm, int32_t *inv, void *ws, size_t ws_bytes, void *stream);
+
+/* A whole block of a SWIGLU layer on the residual stream:
+ *   n = w_pre x / rms(x);  logits = router n;  b = layer(n, top-k of logits)
+ *   y = x + alpha gate p(b)       (p with w_post: its norm; NULL: b itself)
+ * i.e. tq_norm_residual, tq_group_gemm, tq_forward_from_logits and
+ * tq_norm_residual on one stream; n and b are rounded to the layer's act,
+ * logits are f32.
+ *   router DEVICE act [K][d_model]; w_pre, w_post DEVICE w_dtype [d_model]
+ *   x, y DEVICE stream_dtype [T][d_model], dense; y may be x
+ *   gate, gate_v as in tq_norm_desc (TQ_GATE_FULL in act)
+ *   topk_ids DEVICE int32 [T][topk], topk_w DEVICE f32 [T][topk]: written
+ *   ws DEVICE, 256-byte aligned, tq_block_workspace_size() bytes
+ * d_model <= 16384.  Errors: those of its steps, checked before any launch. */
+typedef struct {
+  int32_t topk;
+  tq_dtype stream_dtype, w_dtype;
+  int32_t gate;
+  float alpha, eps;
+  const void *w_pre;
+  const void *w_post;
+  const void *router;
+  tq_rows gate_v;
+} tq_block_desc;
+
+tq_status tq_block_workspace_size(const tq_layer *L, int32_t T, int32_t topk, size_t *bytes);
+tq_status tq_block_forward(const tq_layer *L, const tq_block_desc *d, const void *x, int32_t T,
+                           int32_t *topk_ids, float *topk_w, void *y, void *ws, size_t ws_bytes,
+                           void *stream);
+
 /* ---- offline packer ----------------------------------------------------- */
 
 /* Dense expert weights in, one projection's stored form out (the input of

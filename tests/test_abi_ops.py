@@ -200,3 +200,31 @@ def test_tensors_on_the_host_are_refused(L):
                  lambda: tq.fp8_quant_rows(x, x.to(torch.float8_e4m3fn), torch.zeros((4, 1)))):
         with pytest.raises(tq.TileQError, match="not a tensor on a GPU"):
             call()
+
+
+@pytest.mark.parametrize("T,k,K,code", [(-1, 2, 8, 2), (4, 0, 8, 2), (4, 33, 64, 2), (4, 2, 0, 2), (4, 2, 257, 2),
+                                        (1 << 20, 2, 8, 2), (0, 2, 8, 0), (4, 2, 256, 0)])
+def test_group_slots(L, T, k, K, code):
+    n = ctypes.c_size_t()
+    assert L.tq_group_slots_workspace_size(T, k, K, ctypes.byref(n)) == code, L.tq_last_error()
+    assert L.tq_group_slots_workspace_size(T, k, K, None) == 1
+    if code or T == 0:
+        assert L.tq_group_slots(P, T, k, K, P, P, P, P, 1 << 30, None) == code
+        return
+    assert L.tq_group_slots(P, T, k, K, P, P, P, P, n.value - 1, None) == 2
+    assert L.tq_group_slots(P, T, k, K, P, P, P, P + 64, n.value, None) == 1
+    for i in range(4):
+        a = [P] * 5
+        a[i] = None
+        assert L.tq_group_slots(a[0], T, k, K, a[1], a[2], a[3], a[4], n.value, None) == 1
+
+
+def test_block_without_uploads(L):
+    n, h = ctypes.c_size_t(), ctypes.c_void_p()
+    assert L.tq_block_workspace_size(None, 4, 2, ctypes.byref(n)) == 1
+    d = tq.BlockDesc(2, 0, 0, 0, 1.0, 1e-6, P, P, P, tq.Rows(None, 0))
+    assert L.tq_block_forward(None, ctypes.byref(d), P, 4, P, P, P, P, 1 << 30, None) == 1
+    assert L.tq_layer_create(1, 0, 256, 512, 8, ctypes.byref(h)) == 0
+    assert L.tq_block_workspace_size(h, 4, 2, ctypes.byref(n)) == 6
+    assert L.tq_block_forward(h, ctypes.byref(d), P, 4, P, P, P, P, 1 << 30, None) == 6
+    assert L.tq_layer_destroy(h) == 0

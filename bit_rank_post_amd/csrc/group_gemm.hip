@@ -347,6 +347,26 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  // a wave whose part lies past the tile's rows or outputs only loads
+  const bool idle = wn * (NT / WN) >= nrow || m0 + wm * (MT / WM) >= mdim;
+  if (idle) {
+    wait_vm<F8 ? 0 : 2 * OA::NLD + OB::NLD>();
+    bar_nofence();
+    for (int t = 0; t < nstage; t += 6) {
+#pragma unroll
+      for (int u = 0; u < 6; ++u) {
+        if (t + u >= nstage) break;
+        wait_vm<OA::NLD>();
+        bar_nofence();
+        issue_all(t + u + 2, nullptr, rb_[u % 2]);
+        issue_all(t + u + 3, ra_[u % 3], nullptr);
+        want_rows(t + u + 4);
+      }
+    }
+    wait_vm<0>();
+    return;
+  }
+
   if constexpr (F8) {
     // A stage is one k step of 128, one block of scales: the product of a row
     // i of A's fragments with B comes out of the MFMA by itself and enters the

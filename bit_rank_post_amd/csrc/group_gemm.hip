@@ -28,20 +28,26 @@
 
 namespace tq {
 
-// The group with the i-th most rows (ties in order), so that long sums do not
-// start last; in plain order above 64 groups, where each one's share is small.
-__device__ __forceinline__ int longest_first(const GroupArgs& a, int lane, int i) {
-  if (a.groups > 64) return i;
-  int lo = 0, hi = -1;
-  if (lane < a.groups) group_span(a, lane, &lo, &hi);
-  const int n = hi - lo;                // -1 in lanes without a group
-  int rank = 0;
-  for (int l = 0; l < a.groups; ++l) {
-    const int m = __builtin_amdgcn_readlane(n, l);
-    rank += (m > n || (m == n && l < lane)) ? 1 : 0;
+// The i-th group in the order of work, and its rows [lo, hi): first the groups
+// with more than twice the average of rows, so that long sums do not start
+// last, then the others; in plain order above 64 groups, where each one's
+// share is small.
+__device__ __forceinline__ int work_order(const GroupArgs& a, int lane, int i, int* lo, int* hi) {
+  if (a.groups > 64) {
+    group_span(a, i, lo, hi);
+    return i;
   }
-  const uint64_t me = __ballot(lane < a.groups && rank == i);
-  return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)me) - 1);
+  int l = 0, h = 0;
+  if (lane < a.groups) group_span(a, lane, &l, &h);
+  const bool mine = lane < a.groups, heavy = mine && (long)(h - l) * a.groups > 2L * a.rows;
+  const uint64_t first = __ballot(heavy), rest = __ballot(mine && !heavy);
+  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
+  const int rank = heavy ? __popcll(first & below) : __popcll(first) + __popcll(rest & below);
+  const int g = __builtin_amdgcn_readfirstlane(
+      __ffsll((unsigned long long)__ballot(mine && rank == i)) - 1);
+  *lo = __builtin_amdgcn_readlane(l, g);
+  *hi = __builtin_amdgcn_readlane(h, g);
+  return g;
 }
 
 // Two neighbouring fragments of a column hold, in lane group g, outputs 4g ..
@@ -165,9 +171,8 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
     const int gi = c / mtile;
     m0 = (c - gi * mtile) * MT;
     n0 = (li % ntile) * NT;
-    g = longest_first(a, lane, gi);
     int lo, hi;
-    group_span(a, g, &lo, &hi);
+    g = work_order(a, lane, gi, &lo, &hi);
     row0 = __builtin_amdgcn_readfirstlane(lo);
     K = __builtin_amdgcn_readfirstlane(hi - lo);
     nrow = min(NT, ndim - n0);
@@ -238,8 +243,8 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
   // by scalar loads (wave-uniform, counted apart from the loads in flight) a
   // stage ahead of their use.
   constexpr int KR = MODE == GROUP_DW ? 512 / MT : 1, NIDX = OA::NLD * KR;
-  int sidx[NIDX];
-  auto want_rows = [&](int st) {
+  int sidx[NIDX], sidx1[NIDX], sidx2[NIDX];     // (the last two at the start only)
+  auto want_rows_in = [&](int st, int* sidx) {
     if constexpr (MODE == GROUP_DW) {
       if (!gather_k) return;
       const int k = st * KS + wave * NIDX;
@@ -252,6 +257,7 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
       }
     }
   };
+  auto want_rows = [&](int st) { want_rows_in(st, sidx); };
 
   // load i of A (B) of stage st
   auto issue_a = [&](int st, char* buf, int i) {
@@ -315,12 +321,16 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
   // the next stage has landed), and a stage then takes as long as a trip to
   // memory.  Order of the loads: A0 B0 A1 B1 A2 | B2 A3 | B3 A4 | ...
   want_rows(0);
+  want_rows_in(1, sidx1);
+  want_rows_in(2, sidx2);
   issue_all(0, ra_[0], nullptr);
   issue_all(0, nullptr, rb_[0]);
-  want_rows(1);
+#pragma unroll
+  for (int q = 0; q < NIDX; ++q) sidx[q] = sidx1[q];
   issue_all(1, ra_[1], nullptr);
   issue_all(1, nullptr, rb_[1]);
-  want_rows(2);
+#pragma unroll
+  for (int q = 0; q < NIDX; ++q) sidx[q] = sidx2[q];
   issue_all(2, ra_[2], nullptr);
   want_rows(3);
 

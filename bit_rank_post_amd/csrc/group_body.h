@@ -152,4 +152,30 @@ __device__ __forceinline__ bool locate_row_tile(const GroupArgs& a, int lane, in
   return *nrow > 0;
 }
 
+// Four neighbouring outputs at `at`, `left` of which exist.
+__device__ __forceinline__ void store4(const GroupArgs& a, size_t at, const f32x4& v, int left) {
+  if (a.out_dtype == 2) {
+    float* p = reinterpret_cast<float*>(a.out) + at;
+    if (a.vec_out && left >= 4) *reinterpret_cast<f32x4*>(p) = v;
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = v[i];
+    return;
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = v[i];
+    h[i] = a.out_dtype == 0 ? __builtin_bit_cast(uint16_t, (half_t)f) : __builtin_bit_cast(uint16_t, (__bf16)f);
+  }
+  uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + at;
+  if (a.vec_out && left >= 4)
+    *reinterpret_cast<u32x2*>(p) = u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+  else
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = h[i];
+}
+
 }  // namespace tq

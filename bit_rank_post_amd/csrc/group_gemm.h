@@ -32,16 +32,23 @@ struct GroupArgs {
   const float* ws;               // E4M3: [groups][ceil(d_out/128)][ceil(d_in/128)]
 };
 
-// Few rows per group (decode), Y only: 16 outputs x 16 rows per workgroup,
-// waves over k
-void launch_group_rows(const GroupArgs& a, GroupType type, hipStream_t s);
-long group_rows_grid(const GroupArgs& a);
+// Y by waves over k without LDS staging (outputs x rows per workgroup): few
+// rows per group (decode), or few tiles
+enum GroupRows { ROWS_16x16 = 0, ROWS_32x32 = 1 };
+void launch_group_rows(const GroupArgs& a, GroupType type, GroupRows shape, hipStream_t s);
+long group_rows_grid(const GroupArgs& a, GroupRows shape);
 
 // Tile shapes of the LDS kernel (outputs x rows per workgroup).
 enum GroupTile { TILE_256x256 = 0, TILE_128x128 = 1, TILE_128x32 = 2 };
 
 void launch_group_tile(const GroupArgs& a, GroupMode mode, GroupType type, GroupTile tile, hipStream_t s);
-GroupTile choose_group_tile(const GroupArgs& a, GroupMode mode, GroupType type);
+// the kernel for a product, by sizes and type alone
+struct GroupPick {
+  bool rows;                     // launch_group_rows with shape, else launch_group_tile with tile
+  GroupRows shape;
+  GroupTile tile;
+};
+GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type);
 // workgroups that launch_group_tile would start
 long group_tile_grid(const GroupArgs& a, GroupMode mode, GroupTile tile);
 

@@ -576,10 +576,76 @@ long group_tile_grid(const GroupArgs& a, GroupMode mode, GroupTile t) {
   return (mtile * ntile + 7) / 8 * 8;
 }
 
-GroupTile choose_group_tile(const GroupArgs& a, GroupMode mode, GroupType) {
-  const long avg = a.rows / a.groups;
-  if (mode != GROUP_DW && avg <= 48) return TILE_128x32;
-  return group_tile_grid(a, mode, TILE_256x256) >= 256 ? TILE_256x256 : TILE_128x128;
+// Expected tiles of mt x nt (the host does not know the offsets: a group ends
+// in the middle of a tile on average, and has one at least).
+static double tiles(const GroupArgs& a, GroupMode mode, int mt, int nt) {
+  const long mdim = mode == GROUP_Y ? a.d_out : a.d_in;
+  const double m = (double)((mdim + mt - 1) / mt);
+  if (mode == GROUP_DW) return m * a.groups * ((a.d_out + nt - 1) / nt);
+  if (a.groups == 1) return m * (double)(((long)a.rows + nt - 1) / nt);
+  const double some = a.groups < a.rows ? a.groups : a.rows;
+  const double n = (double)a.rows / nt + 0.5 * some;
+  return m * (n > some ? n : some);
+}
+
+// The kernel with the least expected time, in us, from what each measured over
+// products of 1 .. 64 groups, 32 .. 8192 rows and 256 .. 14336 inputs and
+// outputs in bf16 (e4m3 in brackets; a stage is 128 bytes of k):
+//   rows kernels   all operands come through the L2, at 9.5 and 8 TB/s (7, 6)
+//   128 x 32       0.42 a stage (0.36) while all workgroups run at once (512),
+//                  2 (2.8) times that for each 512 otherwise
+//   128 x 128      0.58 a stage (0.75) with one workgroup a CU, 0.68 (1.0) for
+//                  each 256 workgroups beyond
+//   256 x 256      1.6 a stage (2.6) and round of 256 workgroups, 0.8 (1.25)
+//                  when few run; a last round that is not full costs half
+// plus 4 to 8 for start and end, and at least the time to read the experts'
+// weights: 5.5 TB/s without LDS, 4.6 through it.  Both sides of some borders,
+// bf16, us: one group of 64 rows, 4096 -> 4096: 32 x 32 rows kernel 19, 128 x 32
+// 30; 128 rows: 35, 30, 128 x 128 41; 1024 rows: 128 x 32 67, 128 x 128 46, 256 x
+// 256 80; 290 rows in 3 groups, 5824 -> 640: 32 x 32 rows kernel 25, 128 x 32 41;
+// two rows for each of 60 experts, 2048 -> 1408: 16 x 16 rows kernel 56, 128 x 32
+// 75; 16 for each of 8, 4096 -> 4096: 92, 42; 24960 rows in 64 ragged groups,
+// 2048 -> 1408: 128 x 128 222, 256 x 256 183.
+GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
+  const bool f8 = type == GROUP_E4M3;
+  const double K = mode == GROUP_Y ? a.d_in : (mode == GROUP_DX ? a.d_out : (double)a.rows / a.groups);
+  const double stages = mode == GROUP_DW ? K / 64 + 1 : (double)(long)((K * (f8 ? 1 : 2) + 127) / 128);
+  GroupPick best{false, ROWS_16x16, TILE_256x256};
+  double least = 0;
+  auto offer = [&](const GroupPick& p, double us) {
+    if (least == 0 || us < least) {
+      best = p;
+      least = us;
+    }
+  };
+  const double g256 = tiles(a, mode, 256, 256), g128 = tiles(a, mode, 128, 128);
+  const double r256 = g256 / 256;
+  if (mode == GROUP_DW) {
+    // each tile starts and ends by itself: 8 us a round
+    const auto up = [](double v) { return (double)(long)(v + 0.999); };
+    offer({false, ROWS_16x16, TILE_256x256}, up(r256) * (8 + 1.7 * stages));
+    offer({false, ROWS_16x16, TILE_128x128}, up(g128 / 512) * (8 + 1.36 * stages));
+    return best;
+  }
+  const double weights = (double)(a.groups < a.rows ? a.groups : a.rows) * a.d_in * a.d_out * (f8 ? 1 : 2);
+  const auto least_of = [](double us, double memory) { return us > memory ? us : memory; };
+  const double by_lds = weights / 4.6e6, direct = weights / 5.5e6;
+  offer({false, ROWS_16x16, TILE_256x256},
+        least_of(8 + stages * (r256 <= 1 ? (f8 ? 1.25 : 0.8) * (1 + r256) : (f8 ? 2.6 : 1.6) * (r256 + 0.5)), by_lds + 8));
+  offer({false, ROWS_16x16, TILE_128x128},
+        least_of(8 + stages * (g128 <= 256 ? (f8 ? 0.75 : 0.58) : (f8 ? 1.0 : 0.68) * g128 / 256), by_lds + 4));
+  const double g32 = tiles(a, mode, 128, 32) / 512;
+  offer({false, ROWS_16x16, TILE_128x32},
+        least_of(6 + stages * (f8 ? 0.36 : 0.42) * (g32 <= 1 ? 1 : (f8 ? 2.8 : 2) * g32), by_lds));
+  if (mode == GROUP_Y) {
+    const double row = (double)a.d_in * (f8 ? 1 : 2), avg = (double)a.rows / a.groups;
+    const double n16 = avg < 16 ? avg : 16, n32 = avg < 32 ? avg : 32;     // rows that a tile reads
+    offer({true, ROWS_16x16, TILE_256x256},
+          least_of(4 + tiles(a, mode, 16, 16) * (16 + n16) * row / (f8 ? 7e6 : 9.5e6), direct));
+    offer({true, ROWS_32x32, TILE_256x256},
+          least_of(4 + tiles(a, mode, 32, 32) * (32 + n32) * row / (f8 ? 6e6 : 8e6), direct));
+  }
+  return best;
 }
 
 template <typename T, int MODE, int MT, int NT, int WM, int WN>

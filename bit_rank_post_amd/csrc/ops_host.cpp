@@ -110,23 +110,20 @@ void set_out(GroupArgs* a, void* out, long ldo) {
   a->vec_out = ldo % (a->out_dtype == 2 ? 4 : 8) == 0 && aligned(out, 16) ? 1 : 0;
 }
 
-// few rows per group on average: the weights' bytes bound the product
-bool group_few_rows(const GroupArgs& a, GroupMode mode) {
-  return mode == GROUP_Y && a.rows <= 16L * a.groups;
-}
-
 tq_status run_group(const GroupArgs& a, GroupMode mode, GroupType type, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  // (a workgroup holds 1024 threads at most)
-  if (group_few_rows(a, mode) && group_rows_grid(a) <= GRID_MAX / 2) {
-    launch_group_rows(a, type, s);
+  GroupPick p = choose_group(a, mode, type);
+  // (HIP counts a launch's threads in 32 bits; rows kernels have up to 1024)
+  if (p.rows && group_rows_grid(a, p.shape) > GRID_MAX / 2) p = {false, p.shape, TILE_128x32};
+  if (p.rows) {
+    launch_group_rows(a, type, p.shape, s);
     return launched();
   }
-  const GroupTile tile = choose_group_tile(a, mode, type);
-  const long grid = group_tile_grid(a, mode, tile);
+  if (group_tile_grid(a, mode, p.tile) > GRID_MAX) p.tile = TILE_256x256;
+  const long grid = group_tile_grid(a, mode, p.tile);
   if (grid > GRID_MAX)
     return fail(TQ_EUNSUPPORTED, "%ld workgroups: more than one launch takes", grid);
-  launch_group_tile(a, mode, type, tile, s);
+  launch_group_tile(a, mode, type, p.tile, s);
   return launched();
 }
 

@@ -93,6 +93,8 @@ __device__ __forceinline__ void find_row_tile(const GroupArgs& a, int lane, int 
       const int first = __shfl(inc - tiles, l, 64);
       const int glo = __shfl(lo, l, 64), ghi = __shfl(hi, l, 64);
       *g = __builtin_amdgcn_readfirstlane(g0 + l);
+      // (offsets that break the rules may count more tiles than int holds)
+      if (tile < first || tile - first >= __shfl(tiles, l, 64)) break;
       const int r0 = glo + (tile - first) * NT;
       *row0 = __builtin_amdgcn_readfirstlane(r0);
       *nrow = __builtin_amdgcn_readfirstlane(min(NT, ghi - r0));
@@ -138,9 +140,11 @@ __device__ __forceinline__ bool locate_row_tile(const GroupArgs& a, int lane, in
     const int inc = wave_incl_scan_i(tiles, lane);
     if (!take_item(__builtin_amdgcn_readlane(inc, 63), mtile, &it, m)) return false;
     const uint64_t past = __ballot(inc > it);
-    const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+    const int l = past != 0 ? __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1) : 0;
     const int first = __builtin_amdgcn_readlane(inc - tiles, l);
     const int glo = __builtin_amdgcn_readlane(lo, l), ghi = __builtin_amdgcn_readlane(hi, l);
+    // (offsets that break the rules may count more tiles than int holds)
+    if (past == 0 || it < first || it - first >= __builtin_amdgcn_readlane(tiles, l)) return false;
     *g = l;
     *row0 = glo + (it - first) * NT;
     *nrow = min(NT, ghi - *row0);

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
         for (int j = 0; j < FN; ++j) r.x[d][j][h] = bload128(rx, ok ? vx[j] + h * 64u : OOB, so);
       }
       if constexpr (F8) {
-        const float w = __builtin_bit_cast(float, sload(wsp, live ? st : 0));
+        const float w = live ? __builtin_bit_cast(float, sload(wsp, st)) : 0.f;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
           r.s[d][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(

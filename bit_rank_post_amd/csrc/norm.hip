@@ -325,6 +325,15 @@ __global__ __launch_bounds__(ROWS ? 256 : 1024) void norm_backward_kernel(NormAr
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * NTH;
     if (c >= nv) continue;
+    // (one part is the whole sum; dw is 4-byte aligned only)
+    if (a.nparts == 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (a.dw_post != nullptr) a.dw_post[c * 8 + j] = gp[i][j];
+        if (a.dw_next != nullptr) a.dw_next[c * 8 + j] = gn[i][j];
+      }
+      continue;
+    }
     if (a.dw_post != nullptr) store8(a.part + (size_t)part * a.d + c * 8, gp[i]);
     if (a.dw_next != nullptr) store8(a.part + (size_t)(a.nparts + part) * a.d + c * 8, gn[i]);
   }
@@ -392,7 +401,7 @@ static void backward_go(const NormArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((norm_backward_kernel<S, A, false, 1>), dim3(a.nparts), dim3(row_threads(nv, 1)), 0, s, a);
   else
     hipLaunchKernelGGL((norm_backward_kernel<S, A, false, 2>), dim3(a.nparts), dim3(row_threads(nv, 2)), 0, s, a);
-  if (a.dw_post != nullptr || a.dw_next != nullptr)
+  if (a.nparts > 1 && (a.dw_post != nullptr || a.dw_next != nullptr))
     hipLaunchKernelGGL(norm_join_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, s, a);
 }
 

@@ -103,6 +103,11 @@ tq_status check_group(const tq_group_desc* d, bool e4m3, GroupMode mode, tq_dtyp
   return TQ_OK;
 }
 
+tq_status check_apart(const void* out, const void* a, const void* b) {
+  if (out && (out == a || out == b)) return fail(TQ_EINVAL, "the output is one of the operands");
+  return TQ_OK;
+}
+
 // the stride and alignment rule of 16-byte stores
 void set_out(GroupArgs* a, void* out, long ldo) {
   a->out = out;
@@ -208,6 +213,7 @@ tq_status tq_group_gemm(const tq_group_desc* d, const void* x, const void* w, vo
   if (a.rows == 0) return TQ_OK;
   if ((!x && a.x_rows > 0) || !w || !y) return fail(TQ_EINVAL, "NULL buffer");
   if (!aligned(x, 16) || !aligned(w, 16)) return fail(TQ_EINVAL, "x and w must be 16-byte aligned");
+  TRY(check_apart(y, x, w));
   a.x = x;
   a.w = w;
   set_out(&a, y, a.ldy);
@@ -221,6 +227,7 @@ tq_status tq_group_gemm_dx(const tq_group_desc* d, const void* dy, const void* w
   if (a.rows == 0) return TQ_OK;
   if (!dy || !w || !dx) return fail(TQ_EINVAL, "NULL buffer");
   if (!aligned(dy, 16) || !aligned(w, 16)) return fail(TQ_EINVAL, "dy and w must be 16-byte aligned");
+  TRY(check_apart(dx, dy, w));
   a.dy = dy;
   a.w = w;
   set_out(&a, dx, a.ldx);
@@ -234,6 +241,7 @@ tq_status tq_group_gemm_dw(const tq_group_desc* d, const void* dy, const void* x
   if (!dw) return fail(TQ_EINVAL, "dw is NULL");
   if (a.rows > 0 && (!dy || (!x && a.x_rows > 0))) return fail(TQ_EINVAL, "NULL buffer");
   if (!aligned(dy, 16) || !aligned(x, 16)) return fail(TQ_EINVAL, "dy and x must be 16-byte aligned");
+  TRY(check_apart(dw, dy, x));
   a.dy = dy;
   a.x = x;
   set_out(&a, dw, a.d_in);
@@ -248,6 +256,7 @@ tq_status tq_fp8_gemm(const tq_group_desc* d, const void* x, const float* x_scal
   if ((a.x_rows > 0 && (!x || !x_scale)) || !w || !w_scale || !y) return fail(TQ_EINVAL, "NULL buffer");
   if (!aligned(x, 16) || !aligned(w, 16)) return fail(TQ_EINVAL, "x and w must be 16-byte aligned");
   if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return fail(TQ_EINVAL, "scales must be 4-byte aligned");
+  TRY(check_apart(y, x, w));
   a.x = x;
   a.w = w;
   a.xs = x_scale;

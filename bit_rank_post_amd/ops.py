@@ -49,15 +49,18 @@ def _device(fn, *tensors):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream      # the handle alone, without a Stream object
+_entries = {}
 
 
 def _call(fn, dev, stream, *args):
     """Run the C entry with the tensors' device current, on `stream`."""
+    entry = _entries.get(fn)
+    if entry is None:
+        entry = _entries[fn] = getattr(lib(), "tq_" + fn)
     if stream is None:
         stream = _raw_stream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    entry = getattr(lib(), "tq_" + fn)
     if torch.cuda.current_device() == dev:
         status = entry(*args, stream)
     else:

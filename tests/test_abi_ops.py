@@ -65,6 +65,14 @@ def test_group_pointers_types_and_sources(L):
         assert L.tq_group_gemm(d, *args, 0, None) == 1 and b"aligned" in L.tq_last_error()
         assert L.tq_group_gemm_dx(d, *args, 0, None) == 1 and b"aligned" in L.tq_last_error()
         assert L.tq_group_gemm_dw(d, *args, 0, None) == 1 and b"aligned" in L.tq_last_error()
+    for i in (0, 1):
+        args = [P + 4096, P + 8192, P]
+        args[i] = P                                                   # the output in place of an operand
+        assert L.tq_group_gemm(d, *args, 0, None) == 1 and b"operands" in L.tq_last_error()
+        assert L.tq_group_gemm_dx(d, *args, 0, None) == 1 and b"operands" in L.tq_last_error()
+        assert L.tq_group_gemm_dw(d, *args, 0, None) == 1 and b"operands" in L.tq_last_error()
+        f8 = [args[0], P + 64, args[1], P + 64, P]
+        assert L.tq_fp8_gemm(d, *f8, 0, None) == 1 and b"operands" in L.tq_last_error()
     # the gradients read rows of dy
     for kw in (dict(d_out=60), dict(ldy=68)):
         b = ctypes.byref(group(**kw))
@@ -81,7 +89,7 @@ def test_group_pointers_types_and_sources(L):
     # more workgroups than a launch takes
     assert L.tq_group_gemm(ctypes.byref(group(rows=2 ** 31 - 1)), P, P, P, 0, None) == 5
     big = ctypes.byref(group(groups=1, rows=1 << 30, d_in=8, d_out=1 << 20, ldy=1 << 20))
-    assert L.tq_group_gemm(big, P, P, P, 0, None) == 5 and b"launch" in L.tq_last_error()
+    assert L.tq_group_gemm(big, P, P + 4096, P + 8192, 0, None) == 5 and b"launch" in L.tq_last_error()
 
 
 def test_no_rows_is_no_work(L):

@@ -299,3 +299,18 @@ def test_rows_past_32_bit_offsets():
     dw = torch.empty((2, 8, d), device="cuda")
     tq.group_gemm_dw(torch.ones((rows, 8), dtype=torch.float16, device="cuda"), x, dw, off=off)
     assert (dw[0] == 300 + 200).all() and (dw[1] == 400).all()
+
+
+def test_offsets_that_count_too_many_tiles():
+    """Offsets that give every group all rows (so that tiles are counted again
+    and again): still no access outside the arrays."""
+    G, rows, d = 1000, 4096, 64
+    big = torch.full((3 * rows, d), -7.0, dtype=torch.float16, device="cuda")
+    x, y = torch.ones((rows, d), dtype=torch.float16, device="cuda"), big[rows:2 * rows]
+    w = torch.ones((G, d, d), dtype=torch.float16, device="cuda")
+    off = torch.tensor([0, rows] * (G // 2) + [0], dtype=torch.int32, device="cuda")
+    for g, o in ((G, off), (64, off[:65].contiguous())):
+        tq.group_gemm(x, w[:g], y, off=o)
+        tq.group_gemm_dx(x, w[:g], y, off=o)
+    torch.cuda.synchronize()
+    assert (big[:rows] == -7).all() and (big[2 * rows:] == -7).all()

@@ -233,3 +233,28 @@ def test_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_quotients_are_correctly_rounded():
+    """Codes of many quotients next to the borders between codes, at scales from
+    the smallest to the largest: equal to the definition, one by one."""
+    g = gen(8)
+    rows = []
+    for e in (-126, -120, -101, -100, -99, -60, -10, 0, 7, 60, 100, 118):
+        amax = (1 + torch.rand((64, 1), generator=g)) * 2.0 ** e * 448
+        c = ref_scale(amax.clamp(max=3e38))
+        # the middle of two codes, and its neighbours in f32
+        code = torch.randint(1, 127, (64, 128), generator=g).float()
+        man, exp = code % 8, torch.floor(code / 8)
+        val = torch.where(exp > 0, (1 + (man + 0.5) / 8) * torch.exp2(exp - 7), (man + 0.5) * 2.0 ** -9)
+        x = (val.clamp(max=447) * c).to(torch.float32)
+        step = torch.randint(-2, 3, (64, 128), generator=g, dtype=torch.int32)
+        x = (x.view(torch.int32) + step).clamp(min=0).view(torch.float32)
+        x[:, 0] = amax[:, 0].clamp(max=3e38)
+        rows.append(x)
+    x = torch.cat(rows)
+    q, c = torch.zeros(x.shape, dtype=E4M3, device="cuda"), torch.zeros((len(x), 1), device="cuda")
+    tq.fp8_quant_rows(x.cuda(), q, c)
+    rq, rc = quant_rows_ref(x)
+    assert torch.equal(c.cpu(), rc)
+    assert torch.equal(q.float().double().cpu(), rq)

@@ -423,13 +423,17 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
         xs[set][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, xo[j], k * 4u, 0));
     };
     u32x4 fa[RA][2], fb[FN][2];
+    // (both halves of a fragment from one address, 64 bytes apart by the swizzle)
+    const int at_a = kc_at + wm * (MT / WM) * 128, at_b = kc_at + wn * (NT / WN) * 128;
     auto get_a = [&](const char* op, int i) {
-      fa[i % RA][0] = frag_kc(op + wm * (MT / WM) * 128, i, 0);
-      fa[i % RA][1] = frag_kc(op + wm * (MT / WM) * 128, i, 1);
+      const int at = opaque(at_a);
+      fa[i % RA][0] = *reinterpret_cast<const u32x4*>(op + i * 2048 + at);
+      fa[i % RA][1] = *reinterpret_cast<const u32x4*>(op + i * 2048 + (at ^ 64));
     };
     auto get_b = [&](const char* op, int j) {
-      fb[j][0] = frag_kc(op + wn * (NT / WN) * 128, j, 0);
-      fb[j][1] = frag_kc(op + wn * (NT / WN) * 128, j, 1);
+      const int at = opaque(at_b);
+      fb[j][0] = *reinterpret_cast<const u32x4*>(op + j * 2048 + at);
+      fb[j][1] = *reinterpret_cast<const u32x4*>(op + j * 2048 + (at ^ 64));
     };
     get_scales(0, 0);
     get_scales(1, 1);

@@ -314,3 +314,19 @@ def test_offsets_that_count_too_many_tiles():
         tq.group_gemm_dx(x, w[:g], y, off=o)
     torch.cuda.synchronize()
     assert (big[:rows] == -7).all() and (big[2 * rows:] == -7).all()
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("dtype,value", [("f16", 2.0 ** -20), ("f16", 2.0 ** -24), ("bf16", 2.0 ** -128), ("bf16", 2.0 ** -132)])
+def test_subnormal_values_count(rows, dtype, value):
+    """Values below the smallest normal are not lost: sums of powers of two, exact."""
+    dt, d, o = DT[dtype], 64, 16
+    x = torch.full((rows, d), value, dtype=dt, device="cuda")
+    w, one = torch.ones((1, o, d), dtype=dt, device="cuda"), torch.ones((rows, o), dtype=dt, device="cuda")
+    y, dx, dw = (torch.empty(s, device="cuda") for s in ((rows, o), (rows, d), (1, o, d)))
+    tq.group_gemm(x, w, y)
+    tq.group_gemm_dx(one * value, w, dx)
+    tq.group_gemm_dw(one, x, dw)
+    assert (y.double() == d * value).all() and (dx.double() == o * value).all()
+    # a sum of `rows` equal terms of one bit: exact in f32
+    assert (dw.double() == rows * value).all()

@@ -330,3 +330,20 @@ def test_subnormal_values_count(rows, dtype, value):
     assert (y.double() == d * value).all() and (dx.double() == o * value).all()
     # a sum of `rows` equal terms of one bit: exact in f32
     assert (dw.double() == rows * value).all()
+
+
+@pytest.mark.parametrize("G", [63, 64, 65, 130])
+def test_gradients_of_many_groups(G):
+    """Around and above the groups that a wave holds at once, a few of them heavy."""
+    d_in, d_out = 72, 136
+    counts = [(i * 5 % 7 == 0) * (i % 4) + 150 * (i in (3, G - 1)) for i in range(G)]
+    off, rows, x, dy, w, _ = make(counts, d_in, d_out, torch.float16, 10)
+    offd = torch.tensor(off, dtype=torch.int32, device="cuda")
+    dx, dw = torch.empty((rows, d_in), device="cuda"), torch.empty((G, d_out, d_in), device="cuda")
+    tq.group_gemm_dx(dy.cuda(), w.cuda(), dx, off=offd)
+    tq.group_gemm_dw(dy.cuda(), x.cuda(), dw, off=offd)
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        a, b, c = dy[lo:hi].double(), w[e].double(), x[lo:hi].double()
+        check(f"dx {e}", dx[lo:hi], a @ b, d_out * 2.0 ** -23 * (a.abs() @ b.abs()) + half_step(a @ b, torch.float32))
+        ref = a.t() @ c
+        check(f"dw {e}", dw[e], ref, (hi - lo) * 2.0 ** -23 * (a.t().abs() @ c.abs()) + half_step(ref, torch.float32))

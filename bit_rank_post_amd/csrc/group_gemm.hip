@@ -34,8 +34,8 @@
 // (a dense library product of the size: 1.57); without its loads it takes 2.58
 // ms, without its MFMAs 2.49: memory and matrix unit are used to two thirds
 // each (MFMA busy 67 % of the cycles, no LDS bank conflicts) and do not overlap
-// fully.  24960 rows of 64 ragged experts, 2048 -> 1408, f16: 183 us, DX 214 us,
-// DW 282 us; there a round of workgroups that is not full, and 6 us of start
+// fully.  24960 rows of 64 ragged experts, 2048 -> 1408, f16: 175 us, DX 202 us,
+// DW 283 us; there a round of workgroups that is not full, and 6 us of start
 // and end for each tile, count as much.  e4m3, 16384 x 4096 -> 14336: 1.08 ms,
 // 1.78 PFLOP/s; its matrix unit is busy 36 % of the cycles.
 #include "group_body.h"

@@ -266,10 +266,10 @@ tq_status tq_router_topk(const float *logits, int32_t T, int32_t K, int32_t k, i
  * What a model with such layers needs next to tq_forward: experts that are
  * not packed (16-bit, or 8-bit with block scales) with their gradients, and
  * the norms before and after the block.  All calls are asynchronous on
- * `stream`, allocate nothing, keep no state between calls (so calls may run
- * concurrently on any streams, as long as their outputs and workspaces are
- * apart) and can be captured in a HIP graph.  Inputs and outputs may not
- * overlap except where a call says so. */
+ * `stream`, allocate nothing and can be captured in a HIP graph; all but
+ * tq_block_forward keep no state between calls, so they may run concurrently
+ * on any streams, as long as their outputs and workspaces are apart.  Inputs
+ * and outputs may not overlap except where a call says so. */
 
 /* Rows sorted by expert.  Expert g owns rows off[g] .. off[g+1]-1 of the
  * grouped side (the y side): off DEVICE int32 [groups+1], non-decreasing,
@@ -434,7 +434,8 @@ tq_status tq_group_slots(const int32_t *topk_ids, int32_t T, int32_t topk, int32
  *   gate, gate_v as in tq_norm_desc (TQ_GATE_FULL in act)
  *   topk_ids DEVICE int32 [T][topk], topk_w DEVICE f32 [T][topk]: written
  *   ws DEVICE, 256-byte aligned, tq_block_workspace_size() bytes
- * d_model <= 16384.  Errors: those of its steps, checked before any launch. */
+ * d_model <= 16384.  Calls on one layer are ordered by the caller, as for
+ * tq_forward.  Errors: those of its steps, checked before any launch. */
 typedef struct {
   int32_t topk;
   tq_dtype stream_dtype, w_dtype;

@@ -48,15 +48,19 @@ __device__ __forceinline__ float block_scale(uint32_t amax) {
 }
 
 // The correctly rounded quotients v / c of 8 values, as codes.  By Markstein's
-// theorem, with r = 1 / c correctly rounded, q = v r and the exact remainder
-// e = v - q c (one fma), q + e r rounds v / c correctly: two fma and a product
+// method, with r = 1 / c correctly rounded, p = v r and the exact remainder
+// e = v - p c (one fma), p + e r rounds v / c correctly: two fma and a product
 // a value instead of a division each, which bound the kernel (16384 x 4096 in
-// bf16: 53 -> 44 us).  It holds while nothing underflows: e >= 2^-24 v and v
-// matters from c 2^-10 up, so from c = 2^-100 up; below it, and for scales
-// that are no numbers, the divisions are made.
+// bf16: 53 -> 44 us).  e is exact while no bit of it is below 2^-149: it is a
+// multiple of the steps of p and c, and quotients below 2^-11 are zero codes
+// however they are rounded, so p's step is 2^-34 at least, and 2^-34 2^-23 c is
+// 2^-149 from c = 2^-92 up.  (All 2^23 scales from 2^-92 on, and from 1 on, with
+// the three values on either side of each border between two codes: no quotient
+// differs from the division; from 2^-94 on some do.)  Below, and for scales that
+// are no numbers, the divisions are made.
 __device__ __forceinline__ u32x2 quant8(const float v[8], float c) {
   float q[8];
-  if (c >= 0x1p-100f && c <= 3.0e38f) {
+  if (c >= 0x1p-92f && c <= 3.0e38f) {
     const float r = 1.0f / c;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -65,7 +65,8 @@ __device__ __forceinline__ u32x2 quant8(const float v[8], float c) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float p = v[i] * r;
-      q[i] = __builtin_fmaf(__builtin_fmaf(-p, c, v[i]), r, p);
+      // (the negated remainder, so that its zero leaves a quotient of -0 alone)
+      q[i] = __builtin_fmaf(-__builtin_fmaf(p, c, -v[i]), r, p);
     }
   } else {
 #pragma unroll

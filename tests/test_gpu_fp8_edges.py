@@ -59,3 +59,17 @@ def test_quotients_next_to_a_border(amax, v):
     rq, rc = quant_rows_ref(x)
     assert torch.equal(c, rc) and torch.equal(c, ref_scale(x.abs().amax(1, keepdim=True)))
     assert torch.equal(q.float().double(), rq)
+
+
+@pytest.mark.parametrize("amax", [1.0, 2.0 ** -110])
+def test_zeros_keep_their_sign(amax):
+    """-0 / c is -0, and so is what rounds to zero from below."""
+    x = torch.zeros((1, 128))
+    x[0, :6] = torch.tensor([amax, -0.0, 0.0, -amax * 2.0 ** -21, amax * 2.0 ** -21, -amax])
+    want = torch.tensor([0x7E, 0x80, 0x00, 0x80, 0x00, 0xFE], dtype=torch.uint8)
+    q, _ = quantise(x)
+    assert torch.equal(q.view(torch.uint8)[0, :6], want)
+    w = x.cuda()
+    q, c = torch.zeros((1, 128), dtype=E4M3, device="cuda"), torch.zeros((1, 1), device="cuda")
+    tq.fp8_quant_blocks(w, q, c)
+    assert torch.equal(q.cpu().view(torch.uint8)[0, :6], want)

@@ -27,6 +27,7 @@ EXPORTS = ["tq_layer_create", "tq_upload_proj", "tq_upload_shared_expert",
            "tq_abi_version", "tq_layer_set_path", "tq_forward_path", "tq_debug_route", "tq_debug_dequant", "tq_debug_row_bound", "tq_router_topk",
            "tq_profile_enable", "tq_profile_read", "tq_pack_workspace_size", "tq_pack_proj",
            "tq_calibrate_read", "tq_group_gemm", "tq_group_gemm_dx", "tq_group_gemm_dw", "tq_fp8_gemm",
+           "tq_debug_group_kernel",
            "tq_fp8_quant_rows", "tq_fp8_quant_blocks", "tq_norm_residual", "tq_norm_grad_workspace_size",
            "tq_norm_residual_grad", "tq_group_slots_workspace_size", "tq_group_slots",
            "tq_block_workspace_size", "tq_block_forward"]
@@ -135,6 +136,8 @@ def lib():
         L.tq_group_gemm_dx.argtypes = [pg, vp, vp, vp, i32, vp]
         L.tq_group_gemm_dw.argtypes = [pg, vp, vp, vp, i32, vp]
         L.tq_fp8_gemm.argtypes = [pg, vp, vp, vp, vp, vp, i32, vp]
+        pi = ctypes.POINTER(i32)
+        L.tq_debug_group_kernel.argtypes = [pg, i32, pi, pi, pi]
         L.tq_fp8_quant_rows.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp]
         L.tq_fp8_quant_blocks.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
         L.tq_norm_residual.argtypes = [ctypes.POINTER(NormDesc), vp]

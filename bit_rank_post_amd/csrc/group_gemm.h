@@ -37,6 +37,7 @@ struct GroupArgs {
 enum GroupRows { ROWS_16x16 = 0, ROWS_32x32 = 1 };
 void launch_group_rows(const GroupArgs& a, GroupType type, GroupRows shape, hipStream_t s);
 long group_rows_grid(const GroupArgs& a, GroupRows shape);
+void group_rows_shape(GroupRows shape, int* outputs, int* rows);
 
 // Tile shapes of the LDS kernel (outputs x rows per workgroup).
 enum GroupTile { TILE_256x256 = 0, TILE_128x128 = 1, TILE_128x32 = 2 };
@@ -51,5 +52,6 @@ struct GroupPick {
 GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type);
 // workgroups that launch_group_tile would start
 long group_tile_grid(const GroupArgs& a, GroupMode mode, GroupTile tile);
+void group_tile_shape(GroupTile tile, int* outputs, int* rows);
 
 }  // namespace tq

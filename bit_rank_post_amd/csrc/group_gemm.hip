@@ -572,14 +572,14 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
 
 // ---- launch ------------------------------------------------------------------
 
-static void tile_shape(GroupTile t, int* mt, int* nt) {
+void group_tile_shape(GroupTile t, int* mt, int* nt) {
   *mt = t == TILE_256x256 ? 256 : 128;
   *nt = t == TILE_256x256 ? 256 : (t == TILE_128x128 ? 128 : 32);
 }
 
 long group_tile_grid(const GroupArgs& a, GroupMode mode, GroupTile t) {
   int mt, nt;
-  tile_shape(t, &mt, &nt);
+  group_tile_shape(t, &mt, &nt);
   const long mdim = mode == GROUP_Y ? a.d_out : a.d_in;
   const long mtile = (mdim + mt - 1) / mt;
   long ntile;

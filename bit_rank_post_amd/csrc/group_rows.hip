@@ -138,13 +138,13 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
   }
 }
 
-static void rows_shape(GroupRows r, int* mt, int* nt) {
+void group_rows_shape(GroupRows r, int* mt, int* nt) {
   *mt = *nt = r == ROWS_16x16 ? 16 : 32;
 }
 
 long group_rows_grid(const GroupArgs& a, GroupRows shape) {
   int mt, nt;
-  rows_shape(shape, &mt, &nt);
+  group_rows_shape(shape, &mt, &nt);
   const long mtile = (a.d_out + mt - 1) / mt;
   const long ntile = a.groups == 1 ? ((long)a.rows + nt - 1) / nt
                                    : (long)a.rows / nt + (a.groups < a.rows ? a.groups : a.rows);

@@ -115,20 +115,25 @@ void set_out(GroupArgs* a, void* out, long ldo) {
   a->vec_out = ldo % (a->out_dtype == 2 ? 4 : 8) == 0 && aligned(out, 16) ? 1 : 0;
 }
 
-tq_status run_group(const GroupArgs& a, GroupMode mode, GroupType type, void* stream) {
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  GroupPick p = choose_group(a, mode, type);
+// the kernel for a product and its workgroups
+tq_status pick_group(const GroupArgs& a, GroupMode mode, GroupType type, GroupPick* p) {
+  *p = choose_group(a, mode, type);
   // (HIP counts a launch's threads in 32 bits; rows kernels have up to 1024)
-  if (p.rows && group_rows_grid(a, p.shape) > GRID_MAX / 2) p = {false, p.shape, TILE_128x32};
-  if (p.rows) {
-    launch_group_rows(a, type, p.shape, s);
-    return launched();
-  }
-  if (group_tile_grid(a, mode, p.tile) > GRID_MAX) p.tile = TILE_256x256;
-  const long grid = group_tile_grid(a, mode, p.tile);
+  if (p->rows && group_rows_grid(a, p->shape) > GRID_MAX / 2) *p = {false, p->shape, TILE_128x32};
+  if (p->rows) return TQ_OK;
+  if (group_tile_grid(a, mode, p->tile) > GRID_MAX) p->tile = TILE_256x256;
+  const long grid = group_tile_grid(a, mode, p->tile);
   if (grid > GRID_MAX)
     return fail(TQ_EUNSUPPORTED, "%ld workgroups: more than one launch takes", grid);
-  launch_group_tile(a, mode, type, p.tile, s);
+  return TQ_OK;
+}
+
+tq_status run_group(const GroupArgs& a, GroupMode mode, GroupType type, void* stream) {
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  GroupPick p;
+  TRY(pick_group(a, mode, type, &p));
+  if (p.rows) launch_group_rows(a, type, p.shape, s);
+  else launch_group_tile(a, mode, type, p.tile, s);
   return launched();
 }
 
@@ -263,6 +268,22 @@ tq_status tq_fp8_gemm(const tq_group_desc* d, const void* x, const float* x_scal
   a.ws = w_scale;
   set_out(&a, y, a.ldy);
   return run_group(a, GROUP_Y, GROUP_E4M3, stream);
+}
+
+tq_status tq_debug_group_kernel(const tq_group_desc* d, int32_t product, int32_t* outputs, int32_t* rows,
+                                int32_t* staged) {
+  if (product < 0 || product > 3) return fail(TQ_EINVAL, "product = %d outside [0, 3]", product);
+  if (!outputs || !rows || !staged) return fail(TQ_EINVAL, "outputs, rows or staged is NULL");
+  const bool e4m3 = product == 3;
+  const GroupMode mode = product == 1 ? GROUP_DX : product == 2 ? GROUP_DW : GROUP_Y;
+  GroupArgs a{};
+  TRY(check_group(d, e4m3, mode, TQ_F32, &a));
+  GroupPick p;
+  TRY(pick_group(a, mode, e4m3 ? GROUP_E4M3 : d->act == TQ_F16 ? GROUP_F16 : GROUP_BF16, &p));
+  *staged = p.rows ? 0 : 1;
+  if (p.rows) group_rows_shape(p.shape, outputs, rows);
+  else group_tile_shape(p.tile, outputs, rows);
+  return TQ_OK;
 }
 
 tq_status tq_fp8_quant_rows(const void* x, tq_dtype x_dtype, int32_t rows, int32_t d, int64_t ldx, void* q,

@@ -330,6 +330,15 @@ tq_status tq_group_gemm_dw(const tq_group_desc *d, const void *dy, const void *x
 tq_status tq_fp8_gemm(const tq_group_desc *d, const void *x, const float *x_scale, const void *w,
                       const float *w_scale, void *y, tq_dtype y_dtype, void *stream);
 
+/* Test hook: the kernel that a grouped product of these sizes takes.  product:
+ * 0 tq_group_gemm, 1 tq_group_gemm_dx, 2 tq_group_gemm_dw, 3 tq_fp8_gemm.
+ * *outputs x *rows is what a workgroup computes (d_out x rows, dx: d_in x rows,
+ * dw: d_in x d_out); *staged is 1 for the tile kernels (operands through LDS),
+ * 0 for the kernels whose waves share k.  Host only; d's pointers are not read.
+ * Errors: TQ_EINVAL, TQ_ESHAPE, TQ_EUNSUPPORTED as the product itself. */
+tq_status tq_debug_group_kernel(const tq_group_desc *d, int32_t product, int32_t *outputs,
+                                int32_t *rows, int32_t *staged);
+
 /* Quantisation for tq_fp8_gemm.  Of each block: amax = max |v|,
  * c = max(fl32(amax / 448), 2^-126), or 1 when amax = 0;
  * q = e4m3(fl32(v / c)), to nearest even; c is the scale.  A block with a NaN

@@ -361,12 +361,14 @@ def norm_residual_grad(y, dx=None, dy=None, dn=None, b=None, db=None, w_post=Non
     if ws is not None:
         _dense(fn, ws, "ws")
     elif dw_post is not None or dw_next is not None:
+        # allocated with the call's stream current: the pool then hands the memory
+        # on in that stream's order (and keeps it, when the stream is captured)
         need = norm_grad_workspace(T, d)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:          # freed to the pool of the current stream
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device=dev)
-            ws.record_stream(s)
-            s.wait_stream(torch.cuda.current_stream(dev))
+        s = stream
+        if s is not None and not hasattr(s, "cuda_stream"):
+            s = torch.cuda.ExternalStream(s, device=dev)
+        with torch.cuda.stream(s):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _call(fn, dev, stream, ctypes.byref(desc), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
 
 

@@ -151,6 +151,15 @@ tq_status check_rows(const tq_rows& r, const char* name, bool need, int d, tq_dt
   return TQ_OK;
 }
 
+// An output in place of an input: its rows must lie where the input's do, or a
+// row is written while another, not yet read, lies there.
+tq_status check_in_place(const tq_rows& out, long ldo, const char* out_name, const tq_rows& in, long ldi,
+                         const char* in_name, int T) {
+  if (T > 1 && out.p && out.p == in.p && ldo != ldi)
+    return fail(TQ_EINVAL, "%s in place of %s with another row stride (%ld, %ld)", out_name, in_name, ldo, ldi);
+  return TQ_OK;
+}
+
 tq_status check_norm(int T, int d, tq_dtype st, tq_dtype act, tq_dtype w, int gate, float alpha) {
   if (T < 0) return fail(TQ_ESHAPE, "T = %d", T);
   if (d < 8 || d % 8 || d > NORM_D_MAX)
@@ -191,6 +200,8 @@ tq_status check_norm_forward(const tq_norm_desc* d, NormArgs* a) {
   TRY(check_rows(d->y, "y", false, d->d, d->stream_dtype, &a->ld_y));
   TRY(check_rows(d->b, "b", false, d->d, d->act, &a->ld_b));
   TRY(check_rows(d->n, "n", false, d->d, d->act, &a->ld_n));
+  TRY(check_in_place(d->y, a->ld_y, "y", d->x, a->ld_x, "x", d->T));
+  TRY(check_in_place(d->n, a->ld_n, "n", d->b, a->ld_b, "b", d->T));
   TRY(check_gate(d->gate_v, "gate", d->gate, d->d, d->act, d->T > 0, &a->ld_gate));
   TRY(check_vec(d->w_post, "w_post"));
   TRY(check_vec(d->w_next, "w_next"));
@@ -367,6 +378,10 @@ tq_status tq_norm_residual_grad(const tq_norm_grad_desc* d, void* ws, size_t ws_
   TRY(check_rows(d->dn, "dn", false, d->d, d->act, &a.ld_dn));
   TRY(check_rows(d->b, "b", false, d->d, d->act, &a.ld_b));
   TRY(check_rows(d->db, "db", false, d->d, d->act, &a.ld_db));
+  TRY(check_in_place(d->dx, a.ld_dx, "dx", d->dy, a.ld_dy, "dy", d->T));
+  TRY(check_in_place(d->dx, a.ld_dx, "dx", d->y, a.ld_y, "y", d->T));
+  TRY(check_in_place(d->db, a.ld_db, "db", d->dn, a.ld_dn, "dn", d->T));
+  TRY(check_in_place(d->db, a.ld_db, "db", d->b, a.ld_b, "b", d->T));
   TRY(check_gate(d->gate_v, "gate", d->gate, d->d, d->act, rows, &a.ld_gate));
   TRY(check_gate(d->dgate, "dgate", d->gate, d->d, d->act, false, &a.ld_dgate));
   TRY(check_vec(d->w_post, "w_post"));

@@ -366,7 +366,8 @@ tq_status tq_fp8_quant_blocks(const void *w, tq_dtype w_dtype, int32_t groups, i
  *        TQ_GATE_FULL: act [T][ld]
  *   rstd_post, rstd_next DEVICE f32 [T] or NULL: r1 and r2, for the gradients
  * ld in elements, 0 = d; d % 8 == 0, 8 <= d <= 16384, T < 2^22; 16-byte
- * aligned rows and weights.  y may be x, and n may be b.
+ * aligned rows and weights.  y may be x, and n may be b (the same rows, with
+ * the same stride).
  * Errors: TQ_EINVAL (NULL or misaligned pointers, dtypes, a combination that
  * is not one of the above, alpha or eps), TQ_ESHAPE, TQ_EUNSUPPORTED, TQ_EHIP. */
 typedef struct {
@@ -398,10 +399,10 @@ tq_status tq_norm_residual(const tq_norm_desc *d, void *stream);
  *   dx = dy + w_next's norm backward of dn;   the gradient of b follows from
  *   it through alpha, gate and w_post's norm
  *   dw_post, dw_next DEVICE f32 [d], dgate as the gate (f32 per token, or act)
- * dx may be dy (or y), db may be dn (or b).  T = 0 writes zeros to dw_post and
- * dw_next.  ws: DEVICE, 256-byte aligned, tq_norm_grad_workspace_size() bytes,
- * needed when dw_post or dw_next is wanted.  Sums over rows run in a fixed
- * order.  Errors as tq_norm_residual. */
+ * dx may be dy (or y), db may be dn (or b), the same rows with the same stride.
+ * T = 0 writes zeros to dw_post and dw_next.  ws: DEVICE, 256-byte aligned,
+ * tq_norm_grad_workspace_size() bytes, needed when dw_post or dw_next is
+ * wanted.  Sums over rows run in a fixed order.  Errors as tq_norm_residual. */
 typedef struct {
   int32_t T, d;
   tq_dtype stream_dtype, act, w_dtype;

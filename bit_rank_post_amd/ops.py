@@ -21,7 +21,7 @@ from . import (TQ_BF16, TQ_F16, TQ_F32, BlockDesc, GroupDesc, NormDesc, NormGrad
 
 _DT = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16, torch.float32: TQ_F32}
 E4M3 = torch.float8_e4m3fn
-EINVAL, ESHAPE = 1, 2
+EINVAL, ESHAPE, EUNSUPPORTED = 1, 2, 5
 
 
 def _ptr(t):
@@ -46,6 +46,13 @@ def _device(fn, *tensors):
                 _refuse(fn, f"operands on cuda:{dev} and cuda:{d}", EINVAL)
             dev = d
     return dev
+
+
+def _fits(fn, *sizes):
+    """Sizes that the C ABI takes as 32-bit integers (ctypes would cut them)."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            _refuse(fn, f"a size of {n} does not fit 32 bits", EUNSUPPORTED)
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream      # the handle alone, without a Stream object
@@ -118,6 +125,7 @@ def _group_desc(fn, groups, rows, d_in, d_out, act, off, src, src_div, x_rows, l
     _int32(fn, src, "src", rows)
     if src is None and x_rows != rows:
         _refuse(fn, f"x has {x_rows} rows for {rows} grouped rows and no src")
+    _fits(fn, groups, rows, d_in, d_out, src_div, x_rows)
     return GroupDesc(groups, rows, d_in, d_out, act, _ptr(off), _ptr(src), src_div, x_rows, ldx, ldy)
 
 
@@ -195,6 +203,7 @@ def fp8_quant_rows(x, q, scale, stream=None):
     dev = _device(fn, x, q, scale)
     xdt, ldx = _float(fn, x, "x"), _ld(fn, x, "x")
     rows, d = x.shape
+    _fits(fn, rows, d)
     if q.dtype != E4M3 or scale.dtype != torch.float32:
         _refuse(fn, f"q is {q.dtype} and scale {scale.dtype}: float8_e4m3fn and float32", EINVAL)
     _shape(fn, q, "q", rows, d)
@@ -217,6 +226,7 @@ def fp8_quant_blocks(w, q, scale, stream=None):
         _refuse(fn, f"q is {q.dtype} and scale {scale.dtype}: float8_e4m3fn and float32", EINVAL)
     _shape(fn, q, "q", *w.shape)
     o, i = w.shape[-2:]
+    _fits(fn, *w.shape)
     _shape(fn, scale, "scale", *w.shape[:-2], _blocks(o), _blocks(i))
     for name, t in (("w", w), ("q", q), ("scale", scale)):
         _dense(fn, t, name)
@@ -311,6 +321,7 @@ def norm_residual(x, y=None, n=None, b=None, w_post=None, w_next=None, gate=None
                   rstd_next)
     sdt, ldx = _float(fn, x, "x"), _ld(fn, x, "x")
     T, d = x.shape
+    _fits(fn, T, d)
     a = b if b is not None else n
     act = x.dtype if a is None else a.dtype
     if act not in _DT:
@@ -341,6 +352,7 @@ def norm_residual_grad(y, dx=None, dy=None, dn=None, b=None, db=None, w_post=Non
     sdt = _float(fn, y, "y")
     _ld(fn, y, "y")
     T, d = y.shape
+    _fits(fn, T, d)
     a = b if b is not None else dn
     act = y.dtype if a is None else a.dtype
     if act not in _DT:
@@ -375,6 +387,7 @@ def norm_residual_grad(y, dx=None, dy=None, dn=None, b=None, db=None, w_post=Non
 def norm_grad_workspace(T, d):
     """Bytes of workspace of norm_residual_grad."""
     n = ctypes.c_size_t()
+    _fits("norm_grad_workspace_size", T, d)
     _check("tq_norm_grad_workspace_size", lib().tq_norm_grad_workspace_size(T, d, ctypes.byref(n)))
     return n.value
 
@@ -382,6 +395,7 @@ def norm_grad_workspace(T, d):
 def group_slots_workspace(T, topk, K):
     """Bytes of workspace of group_slots."""
     n = ctypes.c_size_t()
+    _fits("group_slots_workspace_size", T, topk, K)
     _check("tq_group_slots_workspace_size", lib().tq_group_slots_workspace_size(T, topk, K, ctypes.byref(n)))
     return n.value
 
@@ -397,6 +411,7 @@ def group_slots(ids, K, off, perm, inv, ws, stream=None):
     if ids.dim() != 2:
         _refuse(fn, "ids must be [T][topk]")
     T, k = ids.shape
+    _fits(fn, T, k, K)
     _int32(fn, ids, "ids", T, k)
     _int32(fn, off, "off", K + 1)
     _int32(fn, perm, "perm", T * k)
@@ -413,6 +428,7 @@ def block_forward(layer, x, y, router, w_pre, topk, ids_out, gates_out, ws, w_po
     dev = _device(fn, x, y, router, w_pre, ids_out, gates_out, ws, w_post, gate)
     act = torch.float16 if layer.act == TQ_F16 else torch.bfloat16
     sdt, T, d = _float(fn, x, "x"), x.shape[0], layer.d_model
+    _fits(fn, T, topk)
     for name, t in (("x", x), ("y", y)):
         _shape(fn, t, name, T, d)
         _dense(fn, t, name)

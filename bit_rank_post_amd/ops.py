@@ -67,6 +67,8 @@ def _call(fn, dev, stream, *args):
     if stream is None:
         stream = _raw_stream(dev)
     elif hasattr(stream, "cuda_stream"):
+        if getattr(stream, "device_index", dev) != dev:
+            _refuse(fn, f"a stream of cuda:{stream.device_index} for operands on cuda:{dev}", EINVAL)
         stream = stream.cuda_stream
     if torch.cuda.current_device() == dev:
         status = entry(*args, stream)

@@ -407,7 +407,8 @@ def group_slots(ids, K, off, perm, inv, ws, stream=None):
     [K + 1], perm int32 [T * topk] (the src of the grouped products, with
     src_div = topk), inv int32 [T * topk] (row of each slot, -1 for an id
     outside [0, K)).  ws: uint8 tensor of group_slots_workspace(T, topk, K)
-    bytes; its first int32 holds the number of dropped slots afterwards."""
+    bytes; its first int32 holds the number of dropped slots afterwards.  Without
+    tokens all offsets are 0."""
     fn = "group_slots"
     dev = _device(fn, ids, off, perm, inv, ws)
     if ids.dim() != 2:
@@ -421,6 +422,13 @@ def group_slots(ids, K, off, perm, inv, ws, stream=None):
     _dense(fn, ws, "ws")
     _call(fn, dev, stream, _ptr(ids), T, k, K, _ptr(off), _ptr(perm), _ptr(inv), _ptr(ws),
           ws.numel() * ws.element_size())
+    if T == 0:                      # the C call writes nothing then
+        s = stream
+        if s is not None and not hasattr(s, "cuda_stream"):
+            s = torch.cuda.ExternalStream(s, device=dev)
+        with torch.cuda.stream(s):
+            off.zero_()
+            ws.view(-1).view(torch.uint8)[:4].zero_()
 
 
 def block_forward(layer, x, y, router, w_pre, topk, ids_out, gates_out, ws, w_post=None, gate=None, alpha=1.0,

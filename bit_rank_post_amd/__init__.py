@@ -174,7 +174,7 @@ def _stream(stream):
 
 # The operators around a layer (defined in ops.py, offered here)
 _OPS = ("group_gemm", "group_gemm_dx", "group_gemm_dw", "fp8_gemm", "fp8_quant_rows",
-        "fp8_quant_blocks", "norm_residual", "norm_residual_grad",
+        "fp8_quant_blocks", "norm_residual", "norm_residual_grad", "norm_grad_workspace",
         "group_slots", "group_slots_workspace")
 
 

@@ -608,7 +608,8 @@ static double tiles(const GroupArgs& a, GroupMode mode, int mt, int nt) {
 
 // The kernel with the least expected time, in us, from what each measured over
 // products of 1 .. 64 groups, 32 .. 8192 rows and 256 .. 14336 inputs and
-// outputs in bf16 (e4m3 in brackets; a stage is 128 bytes of k):
+// outputs in bf16 (e4m3 in brackets; a stage is 128 bytes of k; 256 CUs).
+// Forward:
 //   rows kernels   all operands come through the L2, at 9.5 and 8 TB/s (7, 6)
 //   128 x 32       0.42 a stage (0.36) while all workgroups run at once (512),
 //                  2 (2.8) times that for each 512 otherwise
@@ -624,6 +625,32 @@ static double tiles(const GroupArgs& a, GroupMode mode, int mt, int nt) {
 // two rows for each of 60 experts, 2048 -> 1408: 16 x 16 rows kernel 56, 128 x 32
 // 75; 16 for each of 8, 4096 -> 4096: 92, 42; 24960 rows in 64 ragged groups,
 // 2048 -> 1408: 128 x 128 222, 256 x 256 183.
+// Input gradient (its A is read by transposing reads, twice as many):
+//   128 x 32       as forward
+//   128 x 128      0.64 a stage with one workgroup a CU, 0.51 for each 256 beyond
+//                  (two a CU cover each other's starts)
+//   256 x 256      1.25 a stage and 0.4 more as the round of 256 fills, then 1.65
+//                  and 8 for start and end in each round
+// Both sides, bf16, us, as 128 x 32, 128 x 128, 256 x 256: d_in and d_out 4096, one
+// group of 1 row 29, 43, 74; 512 rows 38, 46, 94; 1024: 69, 51, 95; 2048: 136,
+// 73, 100; 4096: 257, 134, 112; 8192: 491, 261, 219; 2048 rows in 8 groups 192,
+// 87, 119; 8192 in 8: 610, 290, 252; 64 ragged groups, d_in 2048, d_out 1408,
+// 4096 rows: 107, 94, 120; 24960 rows 413, 212, 232 (eight routings of a skewed
+// router: 128 x 128 216 .. 228, 256 x 256 203 .. 260, by whether its tiles just fill
+// four rounds or start a fifth).  (40 products of 1 .. 79
+// groups, 77 .. 24434 rows and 256 .. 8000 inputs and outputs in f16 that the
+// constants were not taken from: the choice is the fastest or within 2 % for 36,
+// within 14 % for all.)
+// Weight gradient, for each round of workgroups that run at once:
+//   128 x 128      8 and 1.36 a stage of 64 rows (512 workgroups)
+//   256 x 256      8 and 1.7 (256)
+// Both sides, bf16, us, as 128 x 128, 256 x 256: 2048 x 2048, one group of 1024
+// rows 21, 31; 8192 rows 104, 170; 4096 x 4096, one group of 256 rows 24, 19;
+// 16384 rows 660, 423; 2048 rows in 2 groups 97, 72; 8192 in 8: 385, 285; 1024 x
+// 2048, 2048 rows in 8 groups 26, 19; 2048 x 1408, 2100 rows in 16 ragged groups 48,
+// 42; 24960 in 64: 299, 255.  The host does not know how uneven the groups are: where
+// one holds a third of 24960 rows and there are few tiles (64 groups, 1024 x 512),
+// its tiles bound the time and the rule is wrong, 81 against 133.
 GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
   const bool f8 = type == GROUP_E4M3;
   const double K = mode == GROUP_Y ? a.d_in : (mode == GROUP_DX ? a.d_out : (double)a.rows / a.groups);
@@ -648,10 +675,17 @@ GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
   const double weights = (double)(a.groups < a.rows ? a.groups : a.rows) * a.d_in * a.d_out * (f8 ? 1 : 2);
   const auto least_of = [](double us, double memory) { return us > memory ? us : memory; };
   const double by_lds = weights / 4.6e6, direct = weights / 5.5e6;
-  offer({false, ROWS_16x16, TILE_256x256},
-        least_of(8 + stages * (r256 <= 1 ? (f8 ? 1.25 : 0.8) * (1 + r256) : (f8 ? 2.6 : 1.6) * (r256 + 0.5)), by_lds + 8));
-  offer({false, ROWS_16x16, TILE_128x128},
-        least_of(8 + stages * (g128 <= 256 ? (f8 ? 0.75 : 0.58) : (f8 ? 1.0 : 0.68) * g128 / 256), by_lds + 4));
+  if (mode == GROUP_DX) {
+    offer({false, ROWS_16x16, TILE_256x256},
+          least_of(r256 <= 1 ? 8 + stages * (1.25 + 0.4 * r256) : 8 * r256 + stages * 1.65 * (r256 + 0.25), by_lds + 8));
+    offer({false, ROWS_16x16, TILE_128x128},
+          least_of(8 + stages * (g128 <= 256 ? 0.64 : 0.51 * g128 / 256), by_lds + 4));
+  } else {
+    offer({false, ROWS_16x16, TILE_256x256},
+          least_of(8 + stages * (r256 <= 1 ? (f8 ? 1.25 : 0.8) * (1 + r256) : (f8 ? 2.6 : 1.6) * (r256 + 0.5)), by_lds + 8));
+    offer({false, ROWS_16x16, TILE_128x128},
+          least_of(8 + stages * (g128 <= 256 ? (f8 ? 0.75 : 0.58) : (f8 ? 1.0 : 0.68) * g128 / 256), by_lds + 4));
+  }
   const double g32 = tiles(a, mode, 128, 32) / 512;
   offer({false, ROWS_16x16, TILE_128x32},
         least_of(6 + stages * (f8 ? 0.36 : 0.42) * (g32 <= 1 ? 1 : (f8 ? 2.8 : 2) * g32), by_lds));

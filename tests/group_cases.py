@@ -17,7 +17,7 @@ CASES = [
     (Y, (256, 256, 1), 16, 6000, 520, 1032), (Y, (256, 256, 1), 70, 9000, 520, 2056),
     (DX, (128, 32, 1), 4, 40, 136, 520), (DX, (128, 32, 1), 70, 40, 136, 520),
     (DX, (128, 128, 1), 4, 9000, 136, 520), (DX, (128, 128, 1), 70, 9000, 136, 520),
-    (DX, (256, 256, 1), 16, 6000, 1032, 520), (DX, (256, 256, 1), 70, 9000, 2056, 520),
+    (DX, (256, 256, 1), 4, 12000, 1032, 456), (DX, (256, 256, 1), 66, 40000, 2040, 4104),
     (DW, (128, 128, 1), 4, 1900, 136, 264), (DW, (128, 128, 1), 66, 9000, 136, 264),
     (DW, (256, 256, 1), 16, 2100, 520, 1032), (DW, (256, 256, 1), 70, 9000, 264, 520),
     (F8, (16, 16, 0), 7, 40, 912, 136), (F8, (16, 16, 0), 70, 40, 912, 136),

@@ -25,19 +25,23 @@
 // the kernel (no host read back); offsets are clamped to 0 .. rows, so no
 // content of `off` or `src` leads to an access outside the arrays.
 //
-// Tile 256 x 256, 8 waves of 128 x 64: per stage 64 KB come in for 8.4 (e4m3:
-// 16.8) million products, at most 64 bytes a clock and CU, in 1024 of the 2048
+// Tile 256 x 256, 8 waves of 128 x 64: per stage 64 KB come in for 4.2 (e4m3:
+// 8.4) million products, at most 64 bytes a clock and CU, in 1024 of the 2048
 // clocks that its MFMAs take; a smaller tile moves more bytes per product
 // (128 x 128: 0.95 PFLOP/s where this one has 1.28).  16x16x32 MFMA reaches 1.9
 // PFLOP/s here on random values (the clock falls under load), 32x32x16 1.3.
-// Measured, bf16, 32768 rows of 8 experts, 4096 -> 14336: 3.04 ms, 1.27 PFLOP/s
+// Measured, bf16, 32768 rows of 8 experts, 4096 -> 14336: 3.06 ms, 1.26 PFLOP/s
 // (a dense library product of the size: 1.57); without its loads it takes 2.58
 // ms, without its MFMAs 2.49: memory and matrix unit are used to two thirds
 // each (MFMA busy 67 % of the cycles, no LDS bank conflicts) and do not overlap
-// fully.  24960 rows of 64 ragged experts, 2048 -> 1408, f16: 175 us, DX 202 us,
-// DW 283 us; there a round of workgroups that is not full, and 6 us of start
-// and end for each tile, count as much.  e4m3, 16384 x 4096 -> 14336: 1.08 ms,
-// 1.78 PFLOP/s; its matrix unit is busy 36 % of the cycles.
+// fully.  24960 rows of 64 ragged experts, 2048 -> 1408, f16: 183 us, DX (128 x
+// 128) 219 us, DW 282 us; there a round of workgroups that is not full, and 6 us
+// of start and end for each tile, count as much.  e4m3, 16384 x 4096 -> 14336:
+// 1.09 ms, 1.77 PFLOP/s.  A stage of it takes 2.6 us where one of 16 bits, with
+// the same bytes and MFMA clocks, takes 1.6: not the loads hold it.  6.2 vector
+// instructions go with each MFMA (16 bits: 1.1), four of them the fma that need
+// its result: 25 clocks of the vector unit and 32 of the matrix unit in the 88
+// that one MFMA of a SIMD takes (busy 38 % with the MFMAs' issue, and 36 %).
 #include "group_body.h"
 
 namespace tq {

@@ -8,9 +8,10 @@
 // each row a step).  A workgroup takes 16 x 16 or 32 x 32 outputs x rows of one
 // group; its waves share k in interleaved runs of D steps (each requests its
 // next run before it multiplies the last), and their sums are added in LDS in
-// wave order.  60 experts of 2048 -> 1408, 32 tokens top-4, f16: 56 us, 6.2 TB/s
-// of weights (a plain read: 5.5 of a larger buffer); one row through 4096 ->
-// 14336 in e4m3: 14 us, 4.2 TB/s, where the start and the last loads count.
+// wave order.  60 experts of 2048 -> 1408, 32 tokens top-4, f16: 57 us, 5.4 TB/s
+// of the weights of the 53 experts that have rows (a plain read of a larger
+// buffer: 5.5); one row through 4096 -> 14336 in e4m3: 15 us, 4 TB/s, where the
+// start and the last loads count.
 #include "group_body.h"
 
 namespace tq {

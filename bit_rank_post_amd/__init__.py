@@ -30,7 +30,9 @@ EXPORTS = ["tq_layer_create", "tq_upload_proj", "tq_upload_shared_expert",
            "tq_debug_group_kernel",
            "tq_fp8_quant_rows", "tq_fp8_quant_blocks", "tq_norm_residual", "tq_norm_grad_workspace_size",
            "tq_norm_residual_grad", "tq_group_slots_workspace_size", "tq_group_slots",
-           "tq_block_workspace_size", "tq_block_forward"]
+           "tq_block_workspace_size", "tq_block_forward", "tq_int8_gemm", "tq_debug_int8_kernel",
+           "tq_int8_quant_rows", "tq_swiglu", "tq_swiglu_int8", "tq_swiglu_grad", "tq_combine", "tq_combine_grad",
+           "tq_experts_workspace_size", "tq_experts_forward"]
 STAGES = ["route", "row_exponent", "column_stage_in", "gemm_in", "column_stage_down",
           "shared_expert", "gemm_down", "combine"]
 
@@ -99,6 +101,23 @@ class BlockDesc(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("w_pre", "w_post", "router")] + [("gate_v", Rows)])
 
 
+class SwigluDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "ff", "groups", "a_dtype", "h_dtype")]
+                + [("off", ctypes.c_void_p)] + [(n, Rows) for n in ("a", "h", "dh", "da")])
+
+
+class CombineDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "topk", "d", "rows", "z_dtype", "y_dtype")]
+                + [("inv", ctypes.c_void_p), ("w", ctypes.c_void_p)]
+                + [(n, Rows) for n in ("z", "y", "add", "dy", "dz")] + [("dw", ctypes.c_void_p)])
+
+
+class ExpertsDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "topk", "experts", "d", "ff", "act", "y_dtype")]
+                + [(n, ctypes.c_void_p) for n in ("ids", "w", "w_up", "w_down", "s_up", "s_down")]
+                + [(n, Rows) for n in ("x", "y", "add")])
+
+
 _lib = None
 
 
@@ -140,6 +159,17 @@ def lib():
         L.tq_debug_group_kernel.argtypes = [pg, i32, pi, pi, pi]
         L.tq_fp8_quant_rows.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp]
         L.tq_fp8_quant_blocks.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+        L.tq_int8_gemm.argtypes = [pg, vp, vp, vp, vp, vp, i32, vp]
+        L.tq_debug_int8_kernel.argtypes = [pg, pi, pi, pi]
+        L.tq_int8_quant_rows.argtypes = [vp, i32, i32, i32, ctypes.c_int64, vp, vp, vp]
+        ps, pc = ctypes.POINTER(SwigluDesc), ctypes.POINTER(CombineDesc)
+        L.tq_swiglu.argtypes = [ps, vp]
+        L.tq_swiglu_int8.argtypes = [ps, vp, vp, vp]
+        L.tq_swiglu_grad.argtypes = [ps, vp]
+        L.tq_combine.argtypes = [pc, vp]
+        L.tq_combine_grad.argtypes = [pc, vp]
+        L.tq_experts_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.tq_experts_forward.argtypes = [ctypes.POINTER(ExpertsDesc), vp, sz, vp]
         L.tq_norm_residual.argtypes = [ctypes.POINTER(NormDesc), vp]
         L.tq_norm_grad_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
         L.tq_norm_residual_grad.argtypes = [ctypes.POINTER(NormGradDesc), vp, sz, vp]
@@ -175,7 +205,8 @@ def _stream(stream):
 # The operators around a layer (defined in ops.py, offered here)
 _OPS = ("group_gemm", "group_gemm_dx", "group_gemm_dw", "fp8_gemm", "fp8_quant_rows",
         "fp8_quant_blocks", "norm_residual", "norm_residual_grad", "norm_grad_workspace",
-        "group_slots", "group_slots_workspace")
+        "group_slots", "group_slots_workspace", "int8_quant_rows", "int8_gemm", "swiglu", "swiglu_int8",
+        "swiglu_grad", "combine", "combine_grad", "experts_forward", "experts_workspace")
 
 
 def __getattr__(name):

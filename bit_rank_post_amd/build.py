@@ -27,6 +27,7 @@ SOURCES = [("route.hip", "route", []), ("colproj.hip", "colproj", []),
            ("combine.hip", "combine", []), ("upload.hip", "upload", []),
            ("router.hip", "router", []), ("pack.hip", "pack", []), ("calib.hip", "calib", []),
            ("group_gemm.hip", "group_gemm", []), ("group_rows.hip", "group_rows", []), ("quant8.hip", "quant8", []), ("norm.hip", "norm", []),
+           ("swiglu.hip", "swiglu", []), ("slots.hip", "slots", []), ("experts.hip", "experts", []),
            ("tileq_host.cpp", "tileq_host", []), ("ops_host.cpp", "ops_host", [])]
 
 

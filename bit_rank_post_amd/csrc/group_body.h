@@ -7,23 +7,35 @@
 namespace tq {
 
 struct e4m3_t { uint8_t v; };
+struct i8_t { int8_t v; };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 template <typename T> struct Elem { static constexpr int BYTES = 2; };
 template <> struct Elem<e4m3_t> { static constexpr int BYTES = 1; };
+template <> struct Elem<i8_t> { static constexpr int BYTES = 1; };
+
+// sums of products: f32, and of 8-bit integers exact 32-bit integers
+template <typename T> struct Sum { typedef f32x4 type; };
+template <> struct Sum<i8_t> { typedef i32x4 type; };
 
 // 16 elements of k for 16 rows of the A or B operand of one stage half: the
-// 16 bytes of each lane.  16-bit: the operand of one 16x16x32 MFMA.  8-bit:
-// two of them make the operand of one 16x16x128 MFMA (which 32 bytes of k a
-// lane holds is free, as long as A and B agree).
+// 16 bytes of each lane.  16-bit: the operand of one 16x16x32 MFMA; 8-bit
+// integers: of one 16x16x64 MFMA; e4m3: two of them make the operand of one
+// 16x16x128 MFMA (which bytes of k a lane holds is free, as long as A and B
+// agree).
 template <typename T>
-__device__ __forceinline__ f32x4 mfma_half(u32x4 a, u32x4 b, f32x4 c) {
-  typedef typename Vec8<T>::type V8;
-  return mfma16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c);
+__device__ __forceinline__ typename Sum<T>::type mfma_half(u32x4 a, u32x4 b, typename Sum<T>::type c) {
+  if constexpr (sizeof(T) == 1) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+  } else {
+    typedef typename Vec8<T>::type V8;
+    return mfma16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c);
+  }
 }
 
 // The 8-bit matrix instructions add 8 neighbouring products at a time, each
@@ -157,6 +169,29 @@ __device__ __forceinline__ bool locate_row_tile(const GroupArgs& a, int lane, in
   *nrow = __builtin_amdgcn_readfirstlane(*nrow);
   *m = __builtin_amdgcn_readfirstlane(*m);
   return *nrow > 0;
+}
+
+// Products of 8-bit integers: scales of the four outputs o .. o+3 of group g
+// (outputs past the last: 0), and of a row of x (-1: a row of zeros).
+__device__ __forceinline__ f32x4 output_scales(const GroupArgs& a, int g, int o) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  const float* p = a.ws + (size_t)g * a.d_out;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (o + v < a.d_out) s[v] = p[o + v];
+  return s;
+}
+__device__ __forceinline__ float row_scale(const GroupArgs& a, int row) { return row >= 0 ? a.xs[row] : 0.f; }
+
+// The sums of four outputs of one row as they are stored.  8-bit integers:
+// fl32(fl32(fl32(sum) w_scale) x_scale), three roundings in all; the sum is an
+// integer of 1 at least or 0, so its product with a normal scale is one.
+__device__ __forceinline__ f32x4 finish(const f32x4& v, const f32x4&, float) { return v; }
+__device__ __forceinline__ f32x4 finish(const i32x4& v, const f32x4& ws, float xs) {
+  f32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (float)v[i] * ws[i] * xs;
+  return r;
 }
 
 // Four neighbouring outputs at `at`, `left` of which exist.

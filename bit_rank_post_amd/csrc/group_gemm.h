@@ -1,6 +1,6 @@
 // Arguments and launchers of the products grouped by expert (group_gemm.hip,
-// group_rows.hip): 16-bit operands in three directions and 8-bit operands
-// with a scale for each block of 128.
+// group_rows.hip): 16-bit operands in three directions, e4m3 operands with a
+// scale for each block of 128 and 8-bit integers with a scale for each row.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -12,7 +12,7 @@ namespace tq {
 // DX (gradient): dx[r] = W_g^T dy[r]
 // DW (gradient): dW_g  = sum_r dy[r] x[s(r)]^T
 enum GroupMode { GROUP_Y = 0, GROUP_DX = 1, GROUP_DW = 2 };
-enum GroupType { GROUP_F16 = 0, GROUP_BF16 = 1, GROUP_E4M3 = 2 };
+enum GroupType { GROUP_F16 = 0, GROUP_BF16 = 1, GROUP_E4M3 = 2, GROUP_I8 = 3 };
 
 struct GroupArgs {
   int groups, rows, d_in, d_out;
@@ -28,8 +28,8 @@ struct GroupArgs {
   long ldx, ldy, ldo;            // row strides in elements
   int out_dtype;                 // 0 f16, 1 bf16, 2 f32
   int vec_out;                   // eight neighbouring outputs may be stored as 16-byte words
-  const float* xs;               // E4M3: [x_rows][ceil(d_in/128)] scales of x
-  const float* ws;               // E4M3: [groups][ceil(d_out/128)][ceil(d_in/128)]
+  const float* xs;               // E4M3: [x_rows][ceil(d_in/128)] scales of x; I8: [x_rows]
+  const float* ws;               // E4M3: [groups][ceil(d_out/128)][ceil(d_in/128)]; I8: [groups][d_out]
 };
 
 // Y by waves over k without LDS staging (outputs x rows per workgroup): few

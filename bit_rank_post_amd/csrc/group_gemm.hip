@@ -44,6 +44,8 @@
 // that one MFMA of a SIMD takes (busy 38 % with the MFMAs' issue, and 36 %).
 #include "group_body.h"
 
+#include <type_traits>
+
 namespace tq {
 
 // The i-th group in the order of work, and its rows [lo, hi): first the groups
@@ -147,7 +149,8 @@ struct Operand {
 
 template <typename T, int MODE, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
-  constexpr bool F8 = sizeof(T) == 1;
+  constexpr bool F8 = std::is_same<T, e4m3_t>::value, I8 = std::is_same<T, i8_t>::value;
+  typedef typename Sum<T>::type S4;
   constexpr bool AKC = MODE == GROUP_Y, BKC = MODE != GROUP_DW;
   constexpr int ES = Elem<T>::BYTES;
   constexpr int KS = 128 / ES;                  // k per stage
@@ -369,11 +372,11 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
     return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
-  f32x4 acc[FM][FN];
+  S4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) acc[i][j] = S4{0, 0, 0, 0};
 
   // a wave whose part lies past the tile's rows or outputs only loads
   const bool idle = wn * (NT / WN) >= nrow || m0 + wm * (MT / WM) >= mdim;
@@ -558,18 +561,28 @@ __global__ __launch_bounds__(64 * WM * WN) void group_tile_kernel(GroupArgs a) {
   // (every lane takes part in the exchange; rows and columns past the end
   // write nothing)
   static_assert(FM % 2 == 0, "fragments are stored in pairs");
+  f32x4 so[I8 ? FM : 1];
+  if constexpr (I8) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) so[i] = output_scales(a, g, m0 + wm * (MT / WM) + 16 * i + 4 * lg);
+  }
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int n = n0 + wn * (NT / WN) + 16 * j + l16;
     const size_t base = MODE == GROUP_DW ? ((size_t)g * a.d_out + n) * a.d_in : (size_t)(row0 + n) * a.ldo;
     const bool have = n - n0 < nrow;
+    float sr = 0.f;
+    if constexpr (I8) {
+      if (have) sr = row_scale(a, a.src != nullptr ? source_row(a, a.src[row0 + n]) : row0 + n);
+    }
 #pragma unroll
     for (int i = 0; i < FM; i += 2) {
       const int m = m0 + wm * (MT / WM) + 16 * i + 8 * lg;
       const int left = have ? mdim - m : 0;
-      if (a.out_dtype == 2) store8_32(a, base + m, acc[i][j], acc[i + 1][j], left);
-      else if (a.out_dtype == 1) store8_16<true>(a, base + m, acc[i][j], acc[i + 1][j], left);
-      else store8_16<false>(a, base + m, acc[i][j], acc[i + 1][j], left);
+      const f32x4 v = finish(acc[i][j], so[I8 ? i : 0], sr), w = finish(acc[i + 1][j], so[I8 ? i + 1 : 0], sr);
+      if (a.out_dtype == 2) store8_32(a, base + m, v, w, left);
+      else if (a.out_dtype == 1) store8_16<true>(a, base + m, v, w, left);
+      else store8_16<false>(a, base + m, v, w, left);
     }
   }
 }
@@ -657,8 +670,9 @@ static double tiles(const GroupArgs& a, GroupMode mode, int mt, int nt) {
 // its tiles bound the time and the rule is wrong, 81 against 133.
 GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
   const bool f8 = type == GROUP_E4M3;
+  const int es = f8 || type == GROUP_I8 ? 1 : 2;
   const double K = mode == GROUP_Y ? a.d_in : (mode == GROUP_DX ? a.d_out : (double)a.rows / a.groups);
-  const double stages = mode == GROUP_DW ? K / 64 + 1 : (double)(long)((K * (f8 ? 1 : 2) + 127) / 128);
+  const double stages = mode == GROUP_DW ? K / 64 + 1 : (double)(long)((K * es + 127) / 128);
   GroupPick best{false, ROWS_16x16, TILE_256x256};
   double least = 0;
   auto offer = [&](const GroupPick& p, double us) {
@@ -676,7 +690,7 @@ GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
     offer({false, ROWS_16x16, TILE_128x128}, up(g128 / 512) * (8 + 1.36 * stages));
     return best;
   }
-  const double weights = (double)(a.groups < a.rows ? a.groups : a.rows) * a.d_in * a.d_out * (f8 ? 1 : 2);
+  const double weights = (double)(a.groups < a.rows ? a.groups : a.rows) * a.d_in * a.d_out * es;
   const auto least_of = [](double us, double memory) { return us > memory ? us : memory; };
   const double by_lds = weights / 4.6e6, direct = weights / 5.5e6;
   if (mode == GROUP_DX) {
@@ -694,7 +708,7 @@ GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
   offer({false, ROWS_16x16, TILE_128x32},
         least_of(6 + stages * (f8 ? 0.36 : 0.42) * (g32 <= 1 ? 1 : (f8 ? 2.8 : 2) * g32), by_lds));
   if (mode == GROUP_Y) {
-    const double row = (double)a.d_in * (f8 ? 1 : 2), avg = (double)a.rows / a.groups;
+    const double row = (double)a.d_in * es, avg = (double)a.rows / a.groups;
     const double n16 = avg < 16 ? avg : 16, n32 = avg < 32 ? avg : 32;     // rows that a tile reads
     offer({true, ROWS_16x16, TILE_256x256},
           least_of(4 + tiles(a, mode, 16, 16) * (16 + n16) * row / (f8 ? 7e6 : 9.5e6), direct));
@@ -722,6 +736,8 @@ void launch_group_tile(const GroupArgs& a, GroupMode mode, GroupType type, Group
   if (grid <= 0) return;
   if (type == GROUP_E4M3) {
     go_tile<e4m3_t, GROUP_Y>(a, t, grid, s);
+  } else if (type == GROUP_I8) {
+    go_tile<i8_t, GROUP_Y>(a, t, grid, s);
   } else if (type == GROUP_F16) {
     if (mode == GROUP_Y) go_tile<half_t, GROUP_Y>(a, t, grid, s);
     else if (mode == GROUP_DX) go_tile<half_t, GROUP_DX>(a, t, grid, s);

@@ -1,6 +1,6 @@
 // Grouped products y[r][o] = sum_i W_g[o][i] x[s(r)][i] without LDS staging, for
-// decode batches and for products of few tiles; 16-bit operands or e4m3 with
-// block scales.
+// decode batches and for products of few tiles; 16-bit operands, e4m3 with
+// block scales or 8-bit integers with row scales.
 //
 // Bound by the weights' bytes: each weight meets few rows.  So weights go from
 // memory straight to the registers of the one wave that uses them, in the
@@ -14,15 +14,18 @@
 // start and the last loads count.
 #include "group_body.h"
 
+#include <type_traits>
+
 namespace tq {
 
 // A workgroup takes 16 FM outputs x 16 FN rows; a run is D steps of 128 bytes
 // of k: 2 D FM fragment loads of W and 2 D FN of x.
 template <typename T, int WAVES, int FM, int FN, int D>
 __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
-  constexpr bool F8 = sizeof(T) == 1;
+  constexpr bool F8 = std::is_same<T, e4m3_t>::value, I8 = std::is_same<T, i8_t>::value;
+  typedef typename Sum<T>::type S4;
   constexpr int ES = Elem<T>::BYTES, KS = 128 / ES;
-  __shared__ f32x4 s_sum[WAVES > 1 ? WAVES - 1 : 1][FM * FN][64];
+  __shared__ S4 s_sum[WAVES > 1 ? WAVES - 1 : 1][FM * FN][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
@@ -38,6 +41,7 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(
       reinterpret_cast<const char*>(a.x) + (a.src != nullptr ? 0 : (size_t)row0 * a.ldx * ES), (uint32_t)OOB);
   uint32_t vw[FM], vx[FN], vs[FN];
+  int srow[FN];                                 // I8: the row of each column's scale
   const int nkb = (K + 127) >> 7;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -51,6 +55,7 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
     if (row >= 0 && a.src != nullptr) row = source_row(a, a.src[row0 + r]);
     vx[j] = row >= 0 ? (uint32_t)row * (uint32_t)(a.ldx * ES) + lg * 16u : OOB;
     vs[j] = row >= 0 ? (uint32_t)row * nkb * 4u : OOB;
+    srow[j] = row < 0 || a.src != nullptr ? row : row0 + r;
   }
   // scales of this lane's rows and of the outputs' block
   __amdgpu_buffer_rsrc_t rs;
@@ -89,11 +94,11 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
       }
     }
   };
-  f32x4 acc[FM][FN];
+  S4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) acc[i][j] = S4{0, 0, 0, 0};
   auto multiply = [&](const Run& r) {
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -131,11 +136,17 @@ __global__ __launch_bounds__(64 * WAVES) void group_rows_kernel(GroupArgs a) {
   if (wave > 0) return;
 #pragma unroll
   for (int f = 0; f < FM * FN; ++f) {
-    f32x4 v = acc[f / FN][f % FN];
+    S4 v = acc[f / FN][f % FN];
 #pragma unroll
     for (int i = 0; i < WAVES - 1; ++i) v += s_sum[i][f][lane];
     const int r = 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
-    if (r < nrow) store4(a, (size_t)(row0 + r) * a.ldo + o, v, a.d_out - o);
+    f32x4 so = {0.f, 0.f, 0.f, 0.f};
+    float sr = 0.f;
+    if constexpr (I8) {
+      so = output_scales(a, g, o);
+      sr = row_scale(a, srow[f % FN]);
+    }
+    if (r < nrow) store4(a, (size_t)(row0 + r) * a.ldo + o, finish(v, so, sr), a.d_out - o);
   }
 }
 
@@ -179,6 +190,7 @@ void launch_group_rows(const GroupArgs& a, GroupType type, GroupRows shape, hipS
   const long grid = group_rows_grid(a, shape);
   if (grid <= 0) return;
   if (type == GROUP_E4M3) go_rows<e4m3_t>(a, shape, grid, s);
+  else if (type == GROUP_I8) go_rows<i8_t>(a, shape, grid, s);
   else if (type == GROUP_F16) go_rows<half_t>(a, shape, grid, s);
   else go_rows<__bf16>(a, shape, grid, s);
 }

@@ -1,5 +1,6 @@
 // C ABI of the operators around a layer of experts (include/tileq.h): products
-// grouped by expert, 8-bit products with block scales, norms around a block.
+// grouped by expert in 16 and 8 bits, SwiGLU, the sum over slots, a whole layer
+// for a few tokens, norms around a block.
 // Every check runs on the host before any launch; the calls only enqueue
 // kernels on the caller's stream.
 #include <hip/hip_runtime.h>
@@ -10,6 +11,7 @@
 #include <cstdio>
 
 #include "group_gemm.h"
+#include "layer_ops.h"
 #include "norm_ops.h"
 #include "tileq.h"
 #include "tq_internal.h"
@@ -419,6 +421,317 @@ tq_status tq_norm_residual_grad(const tq_norm_grad_desc* d, void* ws, size_t ws_
   a.dw_next = d->dw_next;
   a.part = reinterpret_cast<float*>(ws);
   launch_norm_backward(a, (int)d->stream_dtype, (int)d->act, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+// ---- 8-bit integers ------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+// sums of products of 8-bit codes stay below 2^31: 128^2 * 131071 < 2^31
+constexpr int INT8_D_MAX = 131071;
+tq_status check_int8_group(const tq_group_desc* d, tq_dtype out_dtype, GroupArgs* a) {
+  TRY(check_group(d, true, GROUP_Y, out_dtype, a));
+  if (d->d_in > INT8_D_MAX) return fail(TQ_EUNSUPPORTED, "d_in = %d >= 131072", d->d_in);
+  return TQ_OK;
+}
+tq_status check_int8_rows(int rows, int d, const void* q, const float* scale, bool any) {
+  if (rows < 0) return fail(TQ_ESHAPE, "rows = %d", rows);
+  if (d < 16 || d % 16) return fail(TQ_ESHAPE, "d = %d must be a positive multiple of 16", d);
+  if (d > INT8_D_MAX) return fail(TQ_EUNSUPPORTED, "d = %d >= 131072", d);
+  if (!any) return TQ_OK;
+  if (!q || !scale) return fail(TQ_EINVAL, "NULL buffer");
+  if (!aligned(q, 16) || !aligned(scale, 4)) return fail(TQ_EINVAL, "q must be 16-byte aligned, scale 4-byte");
+  return TQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+tq_status tq_int8_gemm(const tq_group_desc* d, const int8_t* x, const float* x_scale, const int8_t* w,
+                       const float* w_scale, void* y, tq_dtype y_dtype, void* stream) {
+  GroupArgs a{};
+  TRY(check_int8_group(d, y_dtype, &a));
+  if (a.rows == 0) return TQ_OK;
+  if ((a.x_rows > 0 && (!x || !x_scale)) || !w || !w_scale || !y) return fail(TQ_EINVAL, "NULL buffer");
+  if (!aligned(x, 16) || !aligned(w, 16)) return fail(TQ_EINVAL, "x and w must be 16-byte aligned");
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return fail(TQ_EINVAL, "scales must be 4-byte aligned");
+  TRY(check_apart(y, x, w));
+  TRY(check_apart(y, x_scale, w_scale));
+  a.x = x;
+  a.w = w;
+  a.xs = x_scale;
+  a.ws = w_scale;
+  set_out(&a, y, a.ldy);
+  return run_group(a, GROUP_Y, GROUP_I8, stream);
+}
+
+tq_status tq_debug_int8_kernel(const tq_group_desc* d, int32_t* outputs, int32_t* rows, int32_t* staged) {
+  if (!outputs || !rows || !staged) return fail(TQ_EINVAL, "outputs, rows or staged is NULL");
+  GroupArgs a{};
+  TRY(check_int8_group(d, TQ_F32, &a));
+  GroupPick p;
+  TRY(pick_group(a, GROUP_Y, GROUP_I8, &p));
+  *staged = p.rows ? 0 : 1;
+  if (p.rows) group_rows_shape(p.shape, outputs, rows);
+  else group_tile_shape(p.tile, outputs, rows);
+  return TQ_OK;
+}
+
+tq_status tq_int8_quant_rows(const void* x, tq_dtype x_dtype, int32_t rows, int32_t d, int64_t ldx, int8_t* q,
+                             float* scale, void* stream) {
+  if (!is_float(x_dtype)) return fail(TQ_EINVAL, "unknown x_dtype %d", (int)x_dtype);
+  TRY(check_int8_rows(rows, d, q, scale, rows > 0));
+  Int8RowsArgs a{};
+  tq_rows r = {const_cast<void*>(x), ldx};
+  TRY(check_rows(r, "x", rows > 0, d, x_dtype, &a.ldx));
+  if (rows == 0) return TQ_OK;
+  TRY(check_apart(q, x, scale));
+  TRY(check_apart(scale, x, nullptr));
+  a.rows = rows;
+  a.d = d;
+  a.x = x;
+  a.q = q;
+  a.scale = scale;
+  launch_int8_rows(a, (int)x_dtype, false, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+// ---- SwiGLU --------------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+// an output in the place of an input: the same type and stride, or rows are
+// written where others, not yet read, lie
+tq_status check_same_rows(const tq_rows& out, long ldo, tq_dtype to, const char* out_name, const tq_rows& in, long ldi,
+                          tq_dtype ti, const char* in_name) {
+  if (out.p && out.p == in.p && (ldo != ldi || to != ti))
+    return fail(TQ_EINVAL, "%s in place of %s with another type or row stride", out_name, in_name);
+  return TQ_OK;
+}
+tq_status check_swiglu(const tq_swiglu_desc* d, SwigluArgs* a) {
+  if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
+  if (d->rows < 0) return fail(TQ_ESHAPE, "rows = %d", d->rows);
+  if (d->ff < 8 || d->ff % 8 || d->ff > 1 << 24)
+    return fail(TQ_ESHAPE, "ff = %d must be a multiple of 8 from 8 to 2^24", d->ff);
+  if (!is_float(d->a_dtype) || !is_float(d->h_dtype)) return fail(TQ_EINVAL, "unknown dtype");
+  if (d->off && d->groups < 1) return fail(TQ_ESHAPE, "groups = %d", d->groups);
+  if (!aligned(d->off, 4)) return fail(TQ_EINVAL, "off not 4-byte aligned");
+  TRY(check_rows(d->a, "a", d->rows > 0, 2 * d->ff, d->a_dtype, &a->lda));
+  a->rows = d->rows;
+  a->ff = d->ff;
+  a->off = d->off;
+  a->groups = d->groups;
+  a->a = d->a.p;
+  return TQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+tq_status tq_swiglu(const tq_swiglu_desc* d, void* stream) {
+  SwigluArgs a{};
+  TRY(check_swiglu(d, &a));
+  TRY(check_rows(d->h, "h", d->rows > 0, d->ff, d->h_dtype, &a.ldh));
+  TRY(check_same_rows(d->h, a.ldh, d->h_dtype, "h", d->a, a.lda, d->a_dtype, "a"));
+  if (d->rows == 0) return TQ_OK;
+  a.h = d->h.p;
+  launch_swiglu(a, (int)d->a_dtype, (int)d->h_dtype, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+tq_status tq_swiglu_int8(const tq_swiglu_desc* d, int8_t* q, float* scale, void* stream) {
+  SwigluArgs s{};
+  TRY(check_swiglu(d, &s));
+  TRY(check_int8_rows(d->rows, d->ff, q, scale, d->rows > 0));
+  if (d->rows == 0) return TQ_OK;
+  TRY(check_apart(q, s.a, scale));
+  TRY(check_apart(scale, s.a, nullptr));
+  Int8RowsArgs a{};
+  a.rows = s.rows;
+  a.d = s.ff;
+  a.off = s.off;
+  a.groups = s.groups;
+  a.x = s.a;
+  a.ldx = s.lda;
+  a.q = q;
+  a.scale = scale;
+  launch_int8_rows(a, (int)d->a_dtype, true, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+tq_status tq_swiglu_grad(const tq_swiglu_desc* d, void* stream) {
+  SwigluArgs a{};
+  TRY(check_swiglu(d, &a));
+  TRY(check_rows(d->dh, "dh", d->rows > 0, d->ff, d->h_dtype, &a.lddh));
+  TRY(check_rows(d->da, "da", d->rows > 0, 2 * d->ff, d->a_dtype, &a.ldda));
+  TRY(check_rows(d->h, "h", false, d->ff, d->a_dtype, &a.ldh));
+  TRY(check_same_rows(d->da, a.ldda, d->a_dtype, "da", d->a, a.lda, d->a_dtype, "a"));
+  TRY(check_same_rows(d->h, a.ldh, d->a_dtype, "h", d->dh, a.lddh, d->h_dtype, "dh"));
+  if (d->rows == 0) return TQ_OK;
+  TRY(check_apart(d->da.p, d->dh.p, d->h.p));
+  TRY(check_apart(d->h.p, d->a.p, nullptr));
+  a.h = d->h.p;
+  a.dh = d->dh.p;
+  a.da = d->da.p;
+  launch_swiglu_grad(a, (int)d->a_dtype, (int)d->h_dtype, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+// ---- the sum over slots -----------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+tq_status check_combine(const tq_combine_desc* d, SlotSumArgs* a) {
+  if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
+  if (d->T < 0 || d->rows < 0) return fail(TQ_ESHAPE, "T = %d, rows = %d", d->T, d->rows);
+  if (d->topk < 1) return fail(TQ_ESHAPE, "topk = %d", d->topk);
+  if ((long)d->T * d->topk >= 1L << 30) return fail(TQ_EUNSUPPORTED, "%d tokens of %d slots: 2^30 or more", d->T, d->topk);
+  if (d->d < 8 || d->d % 8 || d->d > 1 << 24)
+    return fail(TQ_ESHAPE, "d = %d must be a multiple of 8 from 8 to 2^24", d->d);
+  if (!is_float(d->z_dtype) || !is_float(d->y_dtype)) return fail(TQ_EINVAL, "unknown dtype");
+  if (d->T > 0 && !d->inv) return fail(TQ_EINVAL, "inv is NULL");
+  if (!aligned(d->inv, 4) || !aligned(d->w, 4) || !aligned(d->dw, 4))
+    return fail(TQ_EINVAL, "inv, w and dw must be 4-byte aligned");
+  a->T = d->T;
+  a->topk = d->topk;
+  a->d = d->d;
+  a->rows = d->rows;
+  a->inv = d->inv;
+  a->w = d->w;
+  return TQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+tq_status tq_combine(const tq_combine_desc* d, void* stream) {
+  SlotSumArgs a{};
+  TRY(check_combine(d, &a));
+  TRY(check_rows(d->z, "z", d->T > 0 && d->rows > 0, d->d, d->z_dtype, &a.ldz));
+  TRY(check_rows(d->y, "y", d->T > 0, d->d, d->y_dtype, &a.ldy));
+  TRY(check_rows(d->add, "add", false, d->d, d->y_dtype, &a.ld_add));
+  TRY(check_same_rows(d->y, a.ldy, d->y_dtype, "y", d->add, a.ld_add, d->y_dtype, "add"));
+  if (d->T == 0) return TQ_OK;
+  TRY(check_apart(d->y.p, d->z.p, d->w));
+  a.z = d->z.p;
+  a.y = d->y.p;
+  a.add = d->add.p;
+  launch_slot_sum(a, (int)d->z_dtype, (int)d->y_dtype, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+tq_status tq_combine_grad(const tq_combine_desc* d, void* stream) {
+  SlotSumArgs a{};
+  TRY(check_combine(d, &a));
+  const bool some = d->T > 0 && d->rows > 0;
+  if (d->T > 0 && !d->dz.p && !d->dw) return fail(TQ_EINVAL, "neither dz nor dw is asked for");
+  TRY(check_rows(d->dy, "dy", d->T > 0, d->d, d->y_dtype, &a.ld_dy));
+  TRY(check_rows(d->z, "z", some && d->dw != nullptr, d->d, d->z_dtype, &a.ldz));
+  TRY(check_rows(d->dz, "dz", false, d->d, d->z_dtype, &a.ld_dz));
+  TRY(check_same_rows(d->dz, a.ld_dz, d->z_dtype, "dz", d->z, a.ldz, d->z_dtype, "z"));
+  if (d->T == 0) return TQ_OK;
+  TRY(check_apart(d->dz.p, d->dy.p, d->w));
+  TRY(check_apart(d->dw, d->w, d->dy.p));
+  a.z = d->z.p;
+  a.dy = d->dy.p;
+  a.dz = d->dz.p;
+  a.dw = d->dw;
+  launch_slot_sum_grad(a, (int)d->z_dtype, (int)d->y_dtype, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+// ---- a whole layer for a few tokens ---------------------------------------------
+
+}  // extern "C"
+
+namespace {
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+tq_status check_experts_sizes(int T, int topk, int experts, int d, int ff, int step) {
+  if (T < 0) return fail(TQ_ESHAPE, "T = %d", T);
+  if (topk < 1 || topk > 32) return fail(TQ_ESHAPE, "topk = %d outside [1, 32]", topk);
+  if (experts < 1 || experts > 1024) return fail(TQ_ESHAPE, "experts = %d outside [1, 1024]", experts);
+  if (d < step || d % step || d > 65536) return fail(TQ_ESHAPE, "d = %d must be a multiple of %d up to 65536", d, step);
+  if (ff < step || ff % step || ff > 65536)
+    return fail(TQ_ESHAPE, "ff = %d must be a multiple of %d up to 65536", ff, step);
+  if ((long)T * topk > EXPERTS_SLOTS)
+    return fail(TQ_EUNSUPPORTED, "%d tokens of %d slots: more than %d slots take the grouped products", T, topk,
+                EXPERTS_SLOTS);
+  return TQ_OK;
+}
+struct ExpertsPlan {
+  size_t h, z, bytes;             // counters at 0
+};
+ExpertsPlan plan_experts(int T, int topk, int d, int ff) {
+  ExpertsPlan p;
+  const size_t S = (size_t)T * topk;
+  p.h = up256((size_t)(experts_tiles(d) + 1) * sizeof(int));
+  p.z = p.h + up256(S * ff * 2);
+  p.bytes = p.z + up256(S * d * sizeof(float));
+  return p;
+}
+}  // namespace
+
+extern "C" {
+
+tq_status tq_experts_workspace_size(int32_t T, int32_t topk, int32_t experts, int32_t d, int32_t ff, size_t* bytes) {
+  if (!bytes) return fail(TQ_EINVAL, "bytes is NULL");
+  TRY(check_experts_sizes(T, topk, experts, d, ff, 8));
+  *bytes = plan_experts(T, topk, d, ff).bytes;
+  return TQ_OK;
+}
+
+tq_status tq_experts_forward(const tq_experts_desc* d, void* ws, size_t ws_bytes, void* stream) {
+  if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
+  if (d->act != TQ_F16 && d->act != TQ_BF16) return fail(TQ_EINVAL, "act must be TQ_F16 or TQ_BF16");
+  if (!is_float(d->y_dtype)) return fail(TQ_EINVAL, "unknown y_dtype %d", (int)d->y_dtype);
+  const bool int8 = d->s_up != nullptr;
+  if (int8 != (d->s_down != nullptr)) return fail(TQ_EINVAL, "s_up and s_down go together (8-bit weights)");
+  TRY(check_experts_sizes(d->T, d->topk, d->experts, d->d, d->ff, int8 ? 16 : 8));
+  ExpertsArgs a{};
+  TRY(check_rows(d->x, "x", d->T > 0, d->d, d->act, &a.ldx));
+  if (d->T == 0) return TQ_OK;
+  if (a.ldx * 2 * d->T >= 0x7FFFFFF0L) return fail(TQ_EUNSUPPORTED, "x of %ld bytes >= 2^31", a.ldx * 2 * d->T);
+  a.ldy = d->y.ld ? d->y.ld : d->d;
+  a.ld_add = d->add.ld ? d->add.ld : d->d;
+  if (a.ldy < d->d || a.ld_add < d->d) return fail(TQ_ESHAPE, "row stride of y or add below d = %d", d->d);
+  if (!d->y.p || !d->ids || !d->w || !d->w_up || !d->w_down) return fail(TQ_EINVAL, "NULL buffer");
+  if (!aligned(d->w_up, 16) || !aligned(d->w_down, 16)) return fail(TQ_EINVAL, "weights must be 16-byte aligned");
+  const size_t es = size_of(d->y_dtype);
+  if (!aligned(d->y.p, es) || !aligned(d->add.p, es)) return fail(TQ_EINVAL, "y or add not aligned to its type");
+  if (!aligned(d->ids, 4) || !aligned(d->w, 4) || !aligned(d->s_up, 4) || !aligned(d->s_down, 4))
+    return fail(TQ_EINVAL, "ids, w and scales must be 4-byte aligned");
+  TRY(check_same_rows(d->y, a.ldy, d->y_dtype, "y", d->add, a.ld_add, d->y_dtype, "add"));
+  TRY(check_apart(d->y.p, d->w_up, d->w_down));
+  TRY(check_apart(d->y.p, d->ids, d->w));
+  const ExpertsPlan p = plan_experts(d->T, d->topk, d->d, d->ff);
+  if (!ws) return fail(TQ_EINVAL, "ws is NULL");
+  if (!aligned(ws, 256)) return fail(TQ_EINVAL, "ws not 256-byte aligned");
+  if (ws_bytes < p.bytes) return fail(TQ_ESHAPE, "ws_bytes = %zu < %zu", ws_bytes, p.bytes);
+  a.T = d->T;
+  a.topk = d->topk;
+  a.experts = d->experts;
+  a.d = d->d;
+  a.ff = d->ff;
+  a.ids = d->ids;
+  a.w = d->w;
+  a.x = d->x.p;
+  a.w_up = d->w_up;
+  a.w_down = d->w_down;
+  a.s_up = d->s_up;
+  a.s_down = d->s_down;
+  a.add = d->add.p;
+  a.y = d->y.p;
+  a.ydt = (int)d->y_dtype;
+  char* base = reinterpret_cast<char*>(ws);
+  a.done = reinterpret_cast<int*>(base);
+  a.hit = a.done + experts_tiles(d->d);
+  a.h = base + p.h;
+  a.z = reinterpret_cast<float*>(base + p.z);
+  launch_experts(a, (int)d->act, int8, reinterpret_cast<hipStream_t>(stream));
   return launched();
 }
 

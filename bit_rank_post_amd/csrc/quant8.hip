@@ -14,32 +14,9 @@
 // registers between the maximum and the division.  16384 x 4096 in bf16: 44 us,
 // 4.6 TB/s (a large copy: 5.0).
 #include "norm_ops.h"
-#include "tq_device.h"
+#include "rows.h"
 
 namespace tq {
-
-// 8 neighbouring values as f32 (p 16-byte aligned)
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float v[8]) {
-  typedef typename Vec8<T>::type V8;
-  const V8 r = *reinterpret_cast<const V8*>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)r[i];
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float v[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
-  }
-}
-
-// |v| as bits: ordered like the values, with infinities and then NaN on top
-__device__ __forceinline__ uint32_t abs_bits(float v) {
-  return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
-}
 
 __device__ __forceinline__ float block_scale(uint32_t amax) {
   if (amax == 0) return 1.0f;

@@ -1,0 +1,142 @@
+// The sum over a token's slots after the last product of a layer of experts,
+// and its gradient.
+//
+//   y[t]  = add[t] + sum_j w[t][j] z[inv[t k + j]]         (w = 1 without weights)
+//   dz[inv[t k + j]] = w[t][j] dy[t],  dw[t][j] = dy[t] . z[inv[t k + j]]
+// A slot whose inv lies outside 0 .. rows - 1 was dropped: it adds nothing and
+// its dw is 0.  Sums run in f32, the slots in order, and are rounded once; the
+// sum of a dot product has one fixed order too, so the same inputs give the
+// same bits.  Without weights, y of the rows' gradients is the gradient of
+// gathering them from x.
+//
+// Bound by memory.  Sum: a thread takes 8 values of a token and requests them
+// from four slots at a time.  Gradient: a wave takes a slot, so that few
+// tokens still make many waves; the waves of one token follow each other and
+// find its dy in the cache.
+#include "layer_ops.h"
+#include "rows.h"
+
+namespace tq {
+
+__device__ __forceinline__ int slot_row(const SlotSumArgs& a, int v) { return v >= 0 && v < a.rows ? v : -1; }
+
+template <typename Z, typename Y>
+__global__ __launch_bounds__(256) void slot_sum_kernel(SlotSumArgs a, int t0, uint32_t items, uint32_t nv) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= items) return;
+  const uint32_t r = i / nv;
+  const long t = (long)t0 + r;
+  const int c = (int)(i - r * nv) * 8;
+  const int* inv = a.inv + t * a.topk;
+  const float* w = a.w == nullptr ? nullptr : a.w + t * a.topk;
+  const Z* z = reinterpret_cast<const Z*>(a.z) + c;
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  for (int j0 = 0; j0 < a.topk; j0 += 4) {
+    Raw8<Z> v[4];
+    float g[4];
+    int row[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = j0 + q < a.topk ? slot_row(a, inv[j0 + q]) : -1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (row[q] >= 0) {
+        v[q].load(z + (long)row[q] * a.ldz);
+        g[q] = w == nullptr ? 1.f : w[j0 + q];
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (row[q] >= 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(g[q], v[q].get(e), y[e]);
+      }
+  }
+  if (a.add != nullptr) {
+    float b[8];
+    load8(reinterpret_cast<const Y*>(a.add) + t * a.ld_add + c, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] += b[e];
+  }
+  store8(reinterpret_cast<Y*>(a.y) + t * a.ldy + c, y);
+}
+
+template <typename Z, typename Y>
+__global__ __launch_bounds__(256) void slot_sum_grad_kernel(SlotSumArgs a) {
+  const int lane = threadIdx.x & 63;
+  const long slots = (long)a.T * a.topk, stride = (long)gridDim.x * 4;
+  for (long s = (long)blockIdx.x * 4 + (threadIdx.x >> 6); s < slots; s += stride) {
+    const long t = s / a.topk;
+    const int row = slot_row(a, a.inv[s]);
+    float dot = 0.f;
+    if (row >= 0) {
+      const float g = a.w == nullptr ? 1.f : a.w[s];
+      const Y* dy = reinterpret_cast<const Y*>(a.dy) + t * a.ld_dy;
+      const Z* z = reinterpret_cast<const Z*>(a.z) + (long)row * a.ldz;
+      Z* dz = reinterpret_cast<Z*>(a.dz) + (long)row * a.ld_dz;
+      for (int c0 = 0; c0 < a.d; c0 += 4 * 512) {
+        Raw8<Y> u[4];
+        Raw8<Z> v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = c0 + q * 512 + lane * 8;
+          if (c < a.d) {
+            u[q].load(dy + c);
+            if (a.dw != nullptr) v[q].load(z + c);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = c0 + q * 512 + lane * 8;
+          if (c >= a.d) continue;
+          if (a.dw != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(u[q].get(e), v[q].get(e), dot);
+          }
+          if (a.dz != nullptr) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = g * u[q].get(e);
+            store8(dz + c, o);
+          }
+        }
+      }
+    }
+    if (a.dw != nullptr) {
+      dot = wave_sum(dot);
+      if (lane == 0) a.dw[s] = dot;
+    }
+  }
+}
+
+template <typename Z, typename Y>
+static void go_sum(const SlotSumArgs& a, bool grad, hipStream_t s) {
+  if (grad) {
+    const long slots = (long)a.T * a.topk, groups = (slots + 3) / 4;
+    hipLaunchKernelGGL((slot_sum_grad_kernel<Z, Y>), dim3((unsigned)(groups < (1 << 20) ? groups : 1 << 20)), dim3(256), 0,
+                       s, a);
+    return;
+  }
+  // tokens in parts whose vectors a 32-bit index counts
+  const uint32_t nv = (uint32_t)a.d / 8;
+  const long part = ((1L << 31) - 256) / nv;
+  for (long t0 = 0; t0 < a.T; t0 += part) {
+    const uint32_t n = (uint32_t)(a.T - t0 < part ? a.T - t0 : part);
+    hipLaunchKernelGGL((slot_sum_kernel<Z, Y>), dim3((n * nv + 255) / 256), dim3(256), 0, s, a, (int)t0, n * nv, nv);
+  }
+}
+template <typename Z>
+static void go_sum_y(const SlotSumArgs& a, bool grad, int ydt, hipStream_t s) {
+  if (ydt == 0) go_sum<Z, half_t>(a, grad, s);
+  else if (ydt == 1) go_sum<Z, __bf16>(a, grad, s);
+  else go_sum<Z, float>(a, grad, s);
+}
+static void go_sum_z(const SlotSumArgs& a, bool grad, int zdt, int ydt, hipStream_t s) {
+  if (zdt == 0) go_sum_y<half_t>(a, grad, ydt, s);
+  else if (zdt == 1) go_sum_y<__bf16>(a, grad, ydt, s);
+  else go_sum_y<float>(a, grad, ydt, s);
+}
+void launch_slot_sum(const SlotSumArgs& a, int zdt, int ydt, hipStream_t s) { go_sum_z(a, false, zdt, ydt, s); }
+void launch_slot_sum_grad(const SlotSumArgs& a, int zdt, int ydt, hipStream_t s) { go_sum_z(a, true, zdt, ydt, s); }
+
+}  // namespace tq

@@ -1,6 +1,8 @@
 """Operators around a layer of experts on torch tensors: products grouped by
 expert with their gradients, products in 8-bit floating point with a scale for
-each block of 128, and the norms before and after a block.
+each block of 128 and in 8-bit integers with a scale for each token and channel,
+SwiGLU, the sum over a token's slots, a whole layer for a few tokens, and the
+norms before and after a block.
 
 Argument marshalling and the checks that only tensors allow (shapes, strides,
 dtypes, devices; the C ABI sees pointers); the work runs in the HIP kernels
@@ -16,8 +18,8 @@ import ctypes
 
 import torch
 
-from . import (TQ_BF16, TQ_F16, TQ_F32, BlockDesc, GroupDesc, NormDesc, NormGradDesc, Rows, TileQError, _check,
-               lib)
+from . import (TQ_BF16, TQ_F16, TQ_F32, BlockDesc, CombineDesc, ExpertsDesc, GroupDesc, NormDesc, NormGradDesc,
+               Rows, SwigluDesc, TileQError, _check, lib)
 
 _DT = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16, torch.float32: TQ_F32}
 E4M3 = torch.float8_e4m3fn
@@ -429,6 +431,235 @@ def group_slots(ids, K, off, perm, inv, ws, stream=None):
         with torch.cuda.stream(s):
             off.zero_()
             ws.view(-1).view(torch.uint8)[:4].zero_()
+
+
+def _codes(fn, q, scale, shape):
+    """8-bit codes of the given shape and a scale for each of their rows."""
+    if q.dtype != torch.int8 or scale.dtype != torch.float32:
+        _refuse(fn, f"q is {q.dtype} and scale {scale.dtype}: int8 and float32", EINVAL)
+    _shape(fn, q, "q", *shape)
+    _shape(fn, scale, "scale", *shape[:-1])
+    _dense(fn, q, "q")
+    _dense(fn, scale, "scale")
+
+
+def int8_quant_rows(x, q, scale, stream=None):
+    """x [rows][d] float16, bfloat16 or float32 -> q [rows][d] int8 with a scale
+    for each row, scale float32 [rows].  Weights: x [groups][d_out][d_in]
+    (contiguous), q the same, scale [groups][d_out], one for each output."""
+    fn = "int8_quant_rows"
+    dev = _device(fn, x, q, scale)
+    xdt = _float(fn, x, "x")
+    if x.dim() not in (2, 3):
+        _refuse(fn, "x must be [rows][d] or [groups][d_out][d_in]")
+    _codes(fn, q, scale, tuple(x.shape))
+    if x.dim() == 3:
+        _dense(fn, x, "x")
+        rows, d, ldx = x.shape[0] * x.shape[1], x.shape[2], x.shape[2]
+    else:
+        (rows, d), ldx = x.shape, _ld(fn, x, "x")
+    _fits(fn, rows, d)
+    _call(fn, dev, stream, _ptr(x), xdt, rows, d, ldx, _ptr(q), _ptr(scale))
+
+
+def int8_gemm(x, x_scale, w, w_scale, y, off=None, src=None, src_div=1, stream=None):
+    """The product of group_gemm on operands of int8_quant_rows: x int8 [x_rows]
+    [d_in] with x_scale float32 [x_rows], w int8 [groups][d_out][d_in] (or one
+    matrix) with w_scale float32 [groups][d_out]; y [rows][d_out] float16,
+    bfloat16 or float32.  src gathers the rows of x and of x_scale alike."""
+    fn = "int8_gemm"
+    dev = _device(fn, x, x_scale, w, w_scale, y, off, src)
+    if w.dim() == 2:
+        w, w_scale = w[None], w_scale[None]
+    if w.dim() != 3:
+        _refuse(fn, "w must be [groups][d_out][d_in]")
+    for name, t, dt in (("x", x, torch.int8), ("w", w, torch.int8), ("x_scale", x_scale, torch.float32),
+                        ("w_scale", w_scale, torch.float32)):
+        if t.dtype != dt:
+            _refuse(fn, f"{name} is {t.dtype}, must be {dt}", EINVAL)
+    G, d_out, d_in = w.shape
+    ldx, ldy, ydt = _ld(fn, x, "x"), _ld(fn, y, "y"), _float(fn, y, "y")
+    _shape(fn, x, "x", x.shape[0], d_in)
+    _shape(fn, y, "y", y.shape[0], d_out)
+    _shape(fn, x_scale, "x_scale", x.shape[0])
+    _shape(fn, w_scale, "w_scale", G, d_out)
+    for name, t in (("w", w), ("x_scale", x_scale), ("w_scale", w_scale)):
+        _dense(fn, t, name)
+    d = _group_desc(fn, G, y.shape[0], d_in, d_out, TQ_F16, off, src, src_div, x.shape[0], ldx, ldy)
+    _call(fn, dev, stream, ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y), ydt)
+
+
+def _swiglu_desc(fn, a, off, **mats):
+    """Descriptor of a [rows][2 ff] and matrices of ff or 2 ff columns."""
+    adt, lda = _float(fn, a, "a"), _ld(fn, a, "a")
+    rows, cols = a.shape
+    if cols % 2:
+        _refuse(fn, f"a has {cols} columns: the gate's and as many of the up matrix")
+    groups = 0
+    if off is not None:
+        groups = off.shape[0] - 1 if off.dim() == 1 else 0
+        if groups < 1:
+            _refuse(fn, "off must be [groups + 1]")
+        _int32(fn, off, "off", groups + 1)
+    _fits(fn, rows, cols, groups)
+    d = SwigluDesc(rows, cols // 2, groups, adt, adt, _ptr(off), Rows(a.data_ptr(), lda), _ABSENT, _ABSENT, _ABSENT)
+    for name, (t, width, dtype) in mats.items():
+        setattr(d, name, _mat(fn, t, name, rows, cols // 2 * width, dtype))
+    return d
+
+
+def swiglu(a, h, off=None, stream=None):
+    """h = silu(gate) * up of a [rows][2 ff], the gate's ff columns first: h
+    [rows][ff]; both float16, bfloat16 or float32.  off (int32 [groups + 1], as
+    of group_slots): only rows off[0] .. off[groups] - 1.  h may be a's first
+    half."""
+    fn = "swiglu"
+    dev = _device(fn, a, h, off)
+    hdt = _float(fn, h, "h")
+    d = _swiglu_desc(fn, a, off, h=(h, 1, h.dtype))
+    d.h_dtype = hdt
+    _call(fn, dev, stream, ctypes.byref(d))
+
+
+def swiglu_int8(a, q, scale, off=None, stream=None):
+    """swiglu of a [rows][2 ff] in float32, quantised as by int8_quant_rows: q
+    int8 [rows][ff], scale float32 [rows]."""
+    fn = "swiglu_int8"
+    dev = _device(fn, a, q, scale, off)
+    d = _swiglu_desc(fn, a, off)
+    _codes(fn, q, scale, (d.rows, d.ff))
+    _call(fn, dev, stream, ctypes.byref(d), _ptr(q), _ptr(scale))
+
+
+def swiglu_grad(a, dh, da, h=None, off=None, stream=None):
+    """Gradient of swiglu: da [rows][2 ff] (a's type) of dh [rows][ff] (any of
+    the three types), and with h [rows][ff] (a's type) swiglu's result again.
+    da may be a, and h may be dh."""
+    fn = "swiglu_grad"
+    dev = _device(fn, a, dh, da, h, off)
+    hdt = _float(fn, dh, "dh")
+    d = _swiglu_desc(fn, a, off, dh=(dh, 1, dh.dtype), da=(da, 2, a.dtype), h=(h, 1, a.dtype))
+    d.h_dtype = hdt
+    _call(fn, dev, stream, ctypes.byref(d))
+
+
+def _slots_of(fn, inv, T):
+    """Slots of a token, from inv [T * topk] or [T][topk]."""
+    if inv.dim() == 2:
+        k = inv.shape[1]
+        _shape(fn, inv, "inv", T, k)
+    else:
+        k = inv.numel() // T if T else 1
+        _shape(fn, inv, "inv", T * k)
+    if inv.dtype is not torch.int32:
+        _refuse(fn, f"inv is {inv.dtype}, must be int32", EINVAL)
+    _dense(fn, inv, "inv")
+    return k
+
+
+def _per_slot(fn, t, name, T, k):
+    if t is None:
+        return
+    if t.dtype != torch.float32:
+        _refuse(fn, f"{name} is {t.dtype}, must be float32", EINVAL)
+    _shape(fn, t, name, T, k)
+    _dense(fn, t, name)
+
+
+def combine(z, inv, y, w=None, add=None, stream=None):
+    """y[t] = add[t] + sum over j of w[t][j] * z[inv[t * topk + j]]: z [rows][d]
+    (one row per slot, in expert order), inv int32 [T * topk] of group_slots, w
+    float32 [T][topk] (None: 1), y and add [T][d] of one type.  z and y float16,
+    bfloat16 or float32.  A slot with inv outside [0, rows) adds nothing.  y may
+    be add.  Without w, on the rows of group_gemm_dx: the gradient of x."""
+    fn = "combine"
+    dev = _device(fn, z, inv, y, w, add)
+    zdt, ldz, ydt = _float(fn, z, "z"), _ld(fn, z, "z"), _float(fn, y, "y")
+    rows, d = z.shape
+    T = y.shape[0]
+    k = _slots_of(fn, inv, T)
+    _fits(fn, T, k, d, rows)
+    _per_slot(fn, w, "w", T, k)
+    desc = CombineDesc(T, k, d, rows, zdt, ydt, _ptr(inv), _ptr(w), Rows(z.data_ptr(), ldz),
+                       _mat(fn, y, "y", T, d, y.dtype), _mat(fn, add, "add", T, d, y.dtype), _ABSENT, _ABSENT, None)
+    _call(fn, dev, stream, ctypes.byref(desc))
+
+
+def combine_grad(dy, inv, w=None, z=None, dz=None, dw=None, stream=None):
+    """Gradients of combine: dz[inv[t * topk + j]] = w[t][j] * dy[t] (rows that
+    no slot names are left as they are) and dw[t][j] = dy[t] . z[inv[t * topk +
+    j]] (0 for a slot with inv outside [0, rows)), each None when not wanted;
+    dw needs z.  dz may be z.  The gradient of add is dy."""
+    fn = "combine_grad"
+    dev = _device(fn, dy, inv, w, z, dz, dw)
+    ydt, ld_dy = _float(fn, dy, "dy"), _ld(fn, dy, "dy")
+    T, d = dy.shape
+    k = _slots_of(fn, inv, T)
+    rows_of = z if z is not None else dz
+    if rows_of is None or (dw is not None and z is None):
+        _refuse(fn, "dz or dw is needed, and z for dw", EINVAL)
+    zdt = _float(fn, rows_of, "z" if z is not None else "dz")
+    rows = rows_of.shape[0]
+    _fits(fn, T, k, d, rows)
+    _per_slot(fn, w, "w", T, k)
+    _per_slot(fn, dw, "dw", T, k)
+    desc = CombineDesc(T, k, d, rows, zdt, ydt, _ptr(inv), _ptr(w), _mat(fn, z, "z", rows, d, rows_of.dtype), _ABSENT,
+                       _ABSENT, Rows(dy.data_ptr(), ld_dy), _mat(fn, dz, "dz", rows, d, rows_of.dtype), _ptr(dw))
+    _call(fn, dev, stream, ctypes.byref(desc))
+
+
+def experts_workspace(T, topk, experts, d, ff):
+    """Bytes of workspace of experts_forward."""
+    n = ctypes.c_size_t()
+    _fits("experts_workspace_size", T, topk, experts, d, ff)
+    _check("tq_experts_workspace_size", lib().tq_experts_workspace_size(T, topk, experts, d, ff, ctypes.byref(n)))
+    return n.value
+
+
+def experts_forward(x, ids, w, w_up, w_down, y, ws, s_up=None, s_down=None, add=None, stream=None):
+    """A whole layer of experts for a few tokens (T * topk <= 1024), in two
+    launches: h[t][j] = silu(gate) * up of expert ids[t][j] on x[t], rounded to
+    x's type, and y[t] = add[t] + sum over j of w[t][j] * W_down h[t][j].  x
+    [T][d] float16 or bfloat16; ids int32 [T][topk] (an id outside [0, experts)
+    adds nothing), w float32 [T][topk]; w_up [experts][2 ff][d], the gate's rows
+    first, w_down [experts][d][ff], of x's type or, with s_up float32 [experts]
+    [2 ff] and s_down float32 [experts][d], int8 as of int8_quant_rows; y and
+    add [T][d] float16, bfloat16 or float32 of one type; ws uint8 workspace of
+    experts_workspace(T, topk, experts, d, ff) bytes.  y may be add or x."""
+    fn = "experts_forward"
+    dev = _device(fn, x, ids, w, w_up, w_down, y, ws, s_up, s_down, add)
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        _refuse(fn, f"x is {x.dtype}: float16 or bfloat16", EINVAL)
+    ldx, ldy, ydt = _ld(fn, x, "x"), _ld(fn, y, "y"), _float(fn, y, "y")
+    T, d = x.shape
+    if ids.dim() != 2 or w_up.dim() != 3 or w_down.dim() != 3:
+        _refuse(fn, "ids must be [T][topk], w_up [experts][2 ff][d], w_down [experts][d][ff]")
+    k, (E, _, ff) = ids.shape[1], w_down.shape
+    _fits(fn, T, k, E, d, ff)
+    _int32(fn, ids, "ids", T, k)
+    _per_slot(fn, w, "w", T, k)
+    _shape(fn, y, "y", T, d)
+    _shape(fn, w_up, "w_up", E, 2 * ff, d)
+    _shape(fn, w_down, "w_down", E, d, ff)
+    if (s_up is None) != (s_down is None):
+        _refuse(fn, "s_up and s_down go together", EINVAL)
+    want = x.dtype if s_up is None else torch.int8
+    for name, t in (("w_up", w_up), ("w_down", w_down)):
+        if t.dtype != want:
+            _refuse(fn, f"{name} is {t.dtype}, must be {want}", EINVAL)
+        _dense(fn, t, name)
+    for name, t, n in (("s_up", s_up, 2 * ff), ("s_down", s_down, d)):
+        if t is None:
+            continue
+        if t.dtype != torch.float32:
+            _refuse(fn, f"{name} is {t.dtype}, must be float32", EINVAL)
+        _shape(fn, t, name, E, n)
+        _dense(fn, t, name)
+    _dense(fn, ws, "ws")
+    desc = ExpertsDesc(T, k, E, d, ff, _DT[x.dtype], ydt, _ptr(ids), _ptr(w), _ptr(w_up), _ptr(w_down), _ptr(s_up),
+                       _ptr(s_down), Rows(x.data_ptr(), ldx), Rows(y.data_ptr(), ldy),
+                       _mat(fn, add, "add", T, d, y.dtype))
+    _call(fn, dev, stream, ctypes.byref(desc), _ptr(ws), ws.numel() * ws.element_size())
 
 
 def block_forward(layer, x, y, router, w_pre, topk, ids_out, gates_out, ws, w_post=None, gate=None, alpha=1.0,

@@ -264,8 +264,9 @@ tq_status tq_router_topk(const float *logits, int32_t T, int32_t K, int32_t k, i
 
 /* ---- operators around a layer of experts --------------------------------
  * What a model with such layers needs next to tq_forward: experts that are
- * not packed (16-bit, or 8-bit with block scales) with their gradients, and
- * the norms before and after the block.  All calls are asynchronous on
+ * not packed (16-bit, 8-bit with block scales, or 8-bit integers) with their
+ * gradients, what lies between and after their products, and the norms before
+ * and after the block.  All calls are asynchronous on
  * `stream`, allocate nothing and can be captured in a HIP graph; all but
  * tq_block_forward keep no state between calls, so they may run concurrently
  * on any streams, as long as their outputs and workspaces are apart.  Inputs
@@ -353,6 +354,128 @@ tq_status tq_fp8_quant_rows(const void *x, tq_dtype x_dtype, int32_t rows, int32
 tq_status tq_fp8_quant_blocks(const void *w, tq_dtype w_dtype, int32_t groups, int32_t d_out,
                               int32_t d_in, void *q, float *scale, void *stream);
 
+/* Rows of an operand and their stride in elements. */
+typedef struct {
+  void *p;
+  int64_t ld;
+} tq_rows;
+
+/* The grouped product on 8-bit integers with one f32 scale for each row of x
+ * (token) and each row of w (output channel), as tq_int8_quant_rows makes them:
+ *   y[r][o] = xs[s(r)] ws[g][o] sum_i x[s(r)][i] w[g][o][i]
+ *   x       DEVICE int8 [..][ldx]             x_scale DEVICE f32 [x rows]
+ *   w       DEVICE int8 [groups][d_out][d_in] w_scale DEVICE f32 [groups][d_out]
+ * One group is a plain product.  The sum is exact (32-bit integers; any codes,
+ * -128 among them); y = fl32(fl32(fl32(sum) ws) xs), rounded once more to
+ * y_dtype.  d as for tq_group_gemm (act is not read); d_in and ldx % 16 == 0,
+ * d_in < 131072. */
+tq_status tq_int8_gemm(const tq_group_desc *d, const int8_t *x, const float *x_scale, const int8_t *w,
+                       const float *w_scale, void *y, tq_dtype y_dtype, void *stream);
+
+/* Test hook: the kernel that tq_int8_gemm takes, as tq_debug_group_kernel. */
+tq_status tq_debug_int8_kernel(const tq_group_desc *d, int32_t *outputs, int32_t *rows, int32_t *staged);
+
+/* Quantisation for tq_int8_gemm, of tokens and of weights alike.  Of each row:
+ * amax = max |v|, c = max(fl32(amax / 127), 2^-126), or 1 when amax = 0;
+ * q = rint(fl32(v / c)), ties to even, -127 .. 127; c is the scale.  A row with
+ * a NaN or an infinity gets a scale of NaN and codes of 0.
+ * x DEVICE x_dtype (TQ_F16, TQ_BF16, TQ_F32) [rows][ldx], q DEVICE int8
+ * [rows][d], scale DEVICE f32 [rows].  d % 16 == 0, d < 131072; x and q 16-byte
+ * aligned, rows of x too. */
+tq_status tq_int8_quant_rows(const void *x, tq_dtype x_dtype, int32_t rows, int32_t d, int64_t ldx,
+                             int8_t *q, float *scale, void *stream);
+
+/* SwiGLU between the products of a layer: with a row of a the gate's ff values
+ * and then the up matrix's,
+ *   h = silu(gate) up,  silu(g) = g s,  s = 1 / (1 + e^-g)
+ *   tq_swiglu_int8: its rows quantised as by tq_int8_quant_rows (h in f32)
+ *   tq_swiglu_grad: dgate = dh up s (1 + gate (1 - s)), dup = dh gate s, and h
+ *                   again when h.p is given (for the gradient of the product
+ *                   that read it)
+ * All in f32, rounded once.
+ *   a, da  DEVICE a_dtype [rows][ld], 2 ff values a row
+ *   h      DEVICE [rows][ld]: tq_swiglu h_dtype, tq_swiglu_grad a_dtype
+ *   dh     DEVICE h_dtype [rows][ld]
+ *   off    DEVICE int32 [groups+1] or NULL: only rows off[0] .. off[groups]-1
+ *          (clamped to 0 .. rows) are read and written; NULL: all (groups is
+ *          not read)
+ *   q      DEVICE int8 [rows][ff], scale DEVICE f32 [rows]
+ * ld 0 = dense; ff % 8 == 0 (tq_swiglu_int8: % 16, ff < 131072); rows 16-byte
+ * aligned.  h may be a's first or second half, da may be a, and the gradient's
+ * h may be dh (one type, the same rows with the same stride).
+ * Errors: TQ_EINVAL (NULL or misaligned pointers, dtypes), TQ_ESHAPE, TQ_EHIP. */
+typedef struct {
+  int32_t rows, ff, groups;
+  tq_dtype a_dtype, h_dtype;
+  const int32_t *off;
+  tq_rows a, h, dh, da;
+} tq_swiglu_desc;
+
+tq_status tq_swiglu(const tq_swiglu_desc *d, void *stream);
+tq_status tq_swiglu_int8(const tq_swiglu_desc *d, int8_t *q, float *scale, void *stream);
+tq_status tq_swiglu_grad(const tq_swiglu_desc *d, void *stream);
+
+/* The sum over a token's slots (inv as tq_group_slots writes it):
+ *   y[t] = add[t] + sum_j w[t][j] z[inv[t topk + j]]       (w NULL: 1; add NULL: 0)
+ * and its gradient, each output NULL when not wanted:
+ *   dz[inv[t topk + j]] = w[t][j] dy[t],  dw[t][j] = dy[t] . z[inv[t topk + j]]
+ * A slot whose inv lies outside 0 .. rows-1 adds nothing (whatever its w), and
+ * its dw is 0; rows of dz that no slot names are left as they are.  (Two slots
+ * of one row: dz holds one of the two.)  Sums in f32, in the order of j.
+ * Without w, y of rows of gradients is the gradient of gathering rows from x.
+ *   z, dz DEVICE z_dtype [rows][ld]; y, add, dy DEVICE y_dtype [T][ld], d values
+ *   inv DEVICE int32 [T][topk]; w, dw DEVICE f32 [T][topk]
+ * d % 8 == 0; T topk < 2^30; rows 16-byte aligned; ld 0 = d.  y may be add and
+ * dz may be z (the same rows with the same stride).
+ * Errors: TQ_EINVAL, TQ_ESHAPE, TQ_EUNSUPPORTED, TQ_EHIP. */
+typedef struct {
+  int32_t T, topk, d, rows;
+  tq_dtype z_dtype, y_dtype;
+  const int32_t *inv;
+  const float *w;
+  tq_rows z, y, add, dy, dz;
+  float *dw;
+} tq_combine_desc;
+
+tq_status tq_combine(const tq_combine_desc *d, void *stream);
+tq_status tq_combine_grad(const tq_combine_desc *d, void *stream);
+
+/* A whole layer of experts that are not packed, for a few tokens, in two
+ * launches:
+ *   h[t][j] = RND_act(silu(W_gate,e x_t) W_up,e x_t),  e = ids[t][j]
+ *   y[t]    = add[t] + sum_j w[t][j] W_down,e h[t][j]       (add NULL: 0)
+ *   x      DEVICE act [T][ld] (TQ_F16 or TQ_BF16)
+ *   ids    DEVICE int32 [T][topk], w DEVICE f32 [T][topk]; a slot whose id lies
+ *          outside 0 .. experts-1 adds nothing; an expert may be named twice
+ *   w_up   DEVICE [experts][2 ff][d], the gate's rows first; w_down DEVICE
+ *          [experts][d][ff].  Without scales of type act; with s_up (DEVICE f32
+ *          [experts][2 ff]) and s_down (f32 [experts][d]) 8-bit integers as
+ *          tq_int8_quant_rows makes them, whose value is scale times code (the
+ *          activations stay in 16 bits)
+ *   y, add DEVICE y_dtype [T][ld]
+ *   ws     DEVICE, 256-byte aligned, tq_experts_workspace_size() bytes, of one
+ *          call at a time; its contents before the call do not matter
+ * Sums in f32 in a fixed order.  d and ff % 8 == 0 (8-bit weights: % 16) and
+ * at most 65536; T topk <= 1024 (more tokens: the grouped products); topk <= 32;
+ * experts 1 .. 1024; x below 2^31 bytes, rows of x and weights 16-byte aligned.
+ * y may be add (with the same stride) or x.
+ * Errors: TQ_EINVAL, TQ_ESHAPE, TQ_EUNSUPPORTED (more than 1024 slots), TQ_EHIP. */
+typedef struct {
+  int32_t T, topk, experts, d, ff;
+  tq_dtype act, y_dtype;
+  const int32_t *ids;
+  const float *w;
+  const void *w_up;
+  const void *w_down;
+  const float *s_up;
+  const float *s_down;
+  tq_rows x, y, add;
+} tq_experts_desc;
+
+tq_status tq_experts_workspace_size(int32_t T, int32_t topk, int32_t experts, int32_t d, int32_t ff,
+                                    size_t *bytes);
+tq_status tq_experts_forward(const tq_experts_desc *d, void *ws, size_t ws_bytes, void *stream);
+
 /* Norms before and after a block, with its gate and residual scale:
  *   p(b) = w_post * b * r1,  r1 = (mean(b^2) + eps)^-1/2     (p(b) = b without w_post)
  *   y    = x + alpha * gate * p(b)                            (y = x without b)
@@ -370,11 +493,6 @@ tq_status tq_fp8_quant_blocks(const void *w, tq_dtype w_dtype, int32_t groups, i
  * the same stride).
  * Errors: TQ_EINVAL (NULL or misaligned pointers, dtypes, a combination that
  * is not one of the above, alpha or eps), TQ_ESHAPE, TQ_EUNSUPPORTED, TQ_EHIP. */
-typedef struct {
-  void *p;
-  int64_t ld;
-} tq_rows;
-
 #define TQ_GATE_NONE 0
 #define TQ_GATE_TOKEN 1
 #define TQ_GATE_FULL 2

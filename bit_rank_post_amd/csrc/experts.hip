@@ -8,9 +8,9 @@
 // registers of the one wave that uses them, in the fragment layout of the MFMA
 // (16 outputs x 16 bytes of k a lane).  A workgroup takes 16 outputs of one
 // expert (the up kernel 16 of the gate and the same 16 of the up matrix, whose
-// product it then forms) for all of the expert's slots, 16 FN at a time; its
-// waves share k in interleaved runs of D steps of 128 bytes, each requesting
-// its next run before it multiplies the last, and their sums are added in LDS in
+// product it then forms), or 32 or 64, for all of the expert's slots, 16 FN at a
+// time; its waves share k in interleaved steps of 128 bytes, each requesting its
+// next step before it multiplies the last, and their sums are added in LDS in
 // wave order.  The slots of an expert are found by each workgroup in ids, so
 // nothing runs ahead of the first product.
 //
@@ -87,95 +87,87 @@ __device__ __forceinline__ int find_slots(const ExpertsArgs& a, int unit, int la
   return n;
 }
 
-// Sums of FM x FN fragments over the waves, in wave order; the result goes to
-// wave j for column fragment j.
-template <int WAVES, int FM, int FN>
-__device__ __forceinline__ void join_waves(f32x4 (&acc)[FM][FN], f32x4 (*s_sum)[FM * FN][64], int wave, int lane,
-                                           f32x4 (&sum)[FM]) {
-  static_assert(WAVES >= FN, "a wave for each column fragment");
+// Every wave's FM x FN fragments in LDS, and one of them added over the waves in
+// wave order.
+template <int FM, int FN>
+__device__ __forceinline__ void put_parts(const f32x4 (&acc)[FM][FN], f32x4 (*s_sum)[FM * FN][64], int wave, int lane) {
 #pragma unroll
   for (int f = 0; f < FM * FN; ++f) s_sum[wave][f][lane] = acc[f / FN][f % FN];
   __syncthreads();
-  if (wave < FN) {
+}
+template <int WAVES, int F>
+__device__ __forceinline__ f32x4 sum_parts(const f32x4 (*s_sum)[F][64], int f, int lane) {
+  f32x4 v = s_sum[0][f][lane];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      sum[i] = s_sum[0][i * FN + wave][lane];
-#pragma unroll
-      for (int w = 1; w < WAVES; ++w) sum[i] += s_sum[w][i * FN + wave][lane];
-    }
-  }
+  for (int w = 1; w < WAVES; ++w) v += s_sum[w][f][lane];
+  return v;
 }
 
-// FM fragments of 16 rows of a matrix [..][K] (their bases in wb, rows that
-// exist in wn) times 16 FN columns, whose rows of 16-bit values start xo bytes
+// FM fragments of 16 rows of a matrix [..][K] (their bases in wb, of fragment i
+// rows up to wn[i] exist) times 16 FN columns, whose rows of 16-bit values start xo bytes
 // into xb (OOB: zeros).  The waves share k; acc holds this wave's part.
-template <typename T, bool I8, int WAVES, int FM, int FN, int D>
-__device__ __forceinline__ void part_of_product(const char* const (&wb)[FM], int wn, int K, const char* xb,
+template <typename T, bool I8, int WAVES, int FM, int FN>
+__device__ __forceinline__ void part_of_product(const char* const (&wb)[FM], const int (&wn)[FM], int K, const char* xb,
                                                 const uint32_t (&xo)[FN], int wave, int lane, f32x4 (&acc)[FM][FN]) {
   constexpr int ES = I8 ? 1 : 2, XB = I8 ? 2 : 1;   // bytes of a weight; 16-byte loads of x for one of W
   const int l16 = lane & 15, lg = lane >> 4;
-  const int bytes = K * ES, nstep = (bytes + 127) >> 7, nrun = (nstep + D - 1) / D;
+  const int bytes = K * ES, nstep = (bytes + 127) >> 7;
   __amdgpu_buffer_rsrc_t rw[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) rw[i] = make_rsrc(wb[i], (uint32_t)OOB);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(xb, (uint32_t)OOB);
-  const uint32_t vw = l16 < wn ? (uint32_t)l16 * (uint32_t)bytes + lg * 16u : OOB;
-  struct Run {
-    u32x4 w[D][FM][2], x[D][FN][2][XB];
+  uint32_t vw[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) vw[i] = l16 < wn[i] ? (uint32_t)l16 * (uint32_t)bytes + lg * 16u : OOB;
+  struct Step {
+    u32x4 w[FM][2], x[FN][2][XB];
   };
-  auto fetch = [&](int run, Run& r) {
+  auto fetch = [&](int st, Step& r) {
+    const uint32_t so = st * 128u;
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int st = run * D + d;
-      const bool live = st < nstep;
-      const uint32_t so = live ? st * 128u : 0u;
+    for (int h = 0; h < 2; ++h) {
+      // bytes 64 h + 16 lg of the step's 128: past the row, nothing is read
+      const bool ok = st * 128 + h * 64 + lg * 16 < bytes;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // bytes 64 h + 16 lg of the step's 128: past the row, nothing is read
-        const bool ok = live && st * 128 + h * 64 + lg * 16 < bytes;
+      for (int i = 0; i < FM; ++i) r.w[i][h] = bload128(rw[i], ok ? vw[i] + h * 64u : OOB, so);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) r.w[d][i][h] = bload128(rw[i], ok ? vw + h * 64u : OOB, so);
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int q = 0; q < XB; ++q)
-            r.x[d][j][h][q] = bload128(rx, ok && xo[j] != OOB ? xo[j] + (h * 64u + lg * 16u) * XB + q * 16u : OOB, so * XB);
-      }
+        for (int q = 0; q < XB; ++q)
+          r.x[j][h][q] = bload128(rx, ok && xo[j] != OOB ? xo[j] + (h * 64u + lg * 16u) * XB + q * 16u : OOB, so * XB);
     }
   };
-  auto multiply = [&](const Run& r) {
+  auto multiply = [&](const Step& r) {
 #pragma unroll
-    for (int d = 0; d < D; ++d)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < FM; ++i) {
+        if constexpr (I8) {
+          u32x4 w0, w1;
+          Unpack8<T>::get(r.w[i][h], w0, w1);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          if constexpr (I8) {
-            u32x4 w0, w1;
-            Unpack8<T>::get(r.w[d][i][h], w0, w1);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              acc[i][j] = mfma_half<T>(w0, r.x[d][j][h][0], acc[i][j]);
-              acc[i][j] = mfma_half<T>(w1, r.x[d][j][h][1], acc[i][j]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = mfma_half<T>(r.w[d][i][h], r.x[d][j][h][0], acc[i][j]);
+          for (int j = 0; j < FN; ++j) {
+            acc[i][j] = mfma_half<T>(w0, r.x[j][h][0], acc[i][j]);
+            acc[i][j] = mfma_half<T>(w1, r.x[j][h][1], acc[i][j]);
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = mfma_half<T>(r.w[i][h], r.x[j][h][0], acc[i][j]);
         }
+      }
   };
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Run r0, r1;
-  int run = wave;
-  if (run < nrun) fetch(run, r0);
-  for (; run < nrun; run += 2 * WAVES) {
-    if (run + WAVES < nrun) fetch(run + WAVES, r1);
+  Step r0, r1;
+  int st = wave;
+  if (st < nstep) fetch(st, r0);
+  for (; st < nstep; st += 2 * WAVES) {
+    if (st + WAVES < nstep) fetch(st + WAVES, r1);
     multiply(r0);
-    if (run + WAVES >= nrun) break;
-    if (run + 2 * WAVES < nrun) fetch(run + 2 * WAVES, r0);
+    if (st + WAVES >= nstep) break;
+    if (st + 2 * WAVES < nstep) fetch(st + 2 * WAVES, r0);
     multiply(r1);
   }
 }
@@ -189,10 +181,11 @@ __device__ __forceinline__ f32x4 scales4(const float* p, int o, int n) {
   return s;
 }
 
-template <typename T, bool I8, int WAVES, int FN, int D>
+// 16 P outputs of the gate and the same of the up matrix
+template <typename T, bool I8, int WAVES, int P, int FN>
 __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, int mtile) {
   __shared__ int s_slot[EXPERTS_SLOTS];
-  __shared__ f32x4 s_sum[WAVES][2 * FN][64];
+  __shared__ f32x4 s_sum[WAVES][2 * P * FN][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
@@ -213,7 +206,7 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
     }
     return;
   }
-  const int unit = blockIdx.x / mtile, m0 = (blockIdx.x - unit * mtile) * 16;
+  const int unit = blockIdx.x / mtile, m0 = (blockIdx.x - unit * mtile) * 16 * P;
   int e;
   const int n = __builtin_amdgcn_readfirstlane(find_slots(a, unit, lane, wave, s_slot, &e));
   if (n == 0) return;
@@ -222,7 +215,14 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
 
   constexpr int ES = I8 ? 1 : 2;
   const char* w = reinterpret_cast<const char*>(a.w_up) + ((size_t)e * 2 * a.ff + m0) * a.d * ES;
-  const char* const wb[2] = {w, w + (size_t)a.ff * a.d * ES};
+  const char* wb[2 * P];
+  int wn[2 * P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    wb[p] = w + (size_t)16 * p * a.d * ES;
+    wb[P + p] = wb[p] + (size_t)a.ff * a.d * ES;
+    wn[p] = wn[P + p] = a.ff - m0 - 16 * p;
+  }
   for (int c0 = 0; c0 < n; c0 += 16 * FN) {
     uint32_t xo[FN];
 #pragma unroll
@@ -230,36 +230,38 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
       const int c = c0 + 16 * j + l16;
       xo[j] = c < n ? (uint32_t)(s_slot[c] / a.topk) * (uint32_t)(a.ldx * 2) : OOB;
     }
-    f32x4 acc[2][FN], sum[2];
-    part_of_product<T, I8, WAVES, 2, FN, D>(wb, a.ff - m0, a.d, reinterpret_cast<const char*>(a.x), xo, wave, lane, acc);
+    f32x4 acc[2 * P][FN];
+    part_of_product<T, I8, WAVES, 2 * P, FN>(wb, wn, a.d, reinterpret_cast<const char*>(a.x), xo, wave, lane, acc);
     if (c0 > 0) __syncthreads();
-    join_waves<WAVES, 2, FN>(acc, s_sum, wave, lane, sum);
-    const int c = c0 + 16 * wave + l16, o = m0 + 4 * lg;
-    if (wave >= FN || c >= n || o >= a.ff) continue;
-    if constexpr (I8) {
-      const f32x4 sg = scales4(a.s_up + (size_t)e * 2 * a.ff, o, a.ff), su = scales4(a.s_up + ((size_t)e * 2 + 1) * a.ff, o, a.ff);
-      sum[0] *= sg;
-      sum[1] *= su;
-    }
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    T4 h;
+    put_parts<2 * P, FN>(acc, s_sum, wave, lane);
+    for (int f = wave; f < P * FN; f += WAVES) {
+      const int c = c0 + 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
+      f32x4 g = sum_parts<WAVES, 2 * P * FN>(s_sum, f, lane), u = sum_parts<WAVES, 2 * P * FN>(s_sum, P * FN + f, lane);
+      if (c >= n || o >= a.ff) continue;
+      if constexpr (I8) {
+        g *= scales4(a.s_up + (size_t)e * 2 * a.ff, o, a.ff);
+        u *= scales4(a.s_up + ((size_t)e * 2 + 1) * a.ff, o, a.ff);
+      }
+      typedef T T4 __attribute__((ext_vector_type(4)));
+      T4 h;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) h[v] = (T)(silu_f(sum[0][v]) * sum[1][v]);
-    *reinterpret_cast<T4*>(reinterpret_cast<T*>(a.h) + (size_t)s_slot[c] * a.ff + o) = h;   // ff % 8 == 0
+      for (int v = 0; v < 4; ++v) h[v] = (T)(silu_f(g[v]) * u[v]);
+      *reinterpret_cast<T4*>(reinterpret_cast<T*>(a.h) + (size_t)s_slot[c] * a.ff + o) = h;   // ff % 8 == 0
+    }
   }
 }
 
-// y of 16 outputs from o0: the slots of each token in order
-template <int WAVES>
+// y of M outputs from o0: the slots of each token in order
+template <int WAVES, int M>
 __device__ __forceinline__ void add_slots(const ExpertsArgs& a, int o0, bool any) {
-  for (int i = threadIdx.x; i < a.T * 16; i += 64 * WAVES) {
-    const int t = i >> 4, o = o0 + (i & 15);
+  for (int i = threadIdx.x; i < a.T * M; i += 64 * WAVES) {
+    const int t = i / M, o = o0 + i % M;
     if (o >= a.d) continue;
     float y = 0.f;
     if (any)
       for (int j = 0; j < a.topk; ++j) {
         const int s = t * a.topk + j, e = a.ids[s];
-        if (e >= 0 && e < a.experts) y += a.z[(size_t)s * a.d + o];
+        if (e >= 0 && e < a.experts) y += __hip_atomic_load(a.z + (size_t)s * a.d + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     const size_t at = (size_t)t * a.ldy + o, from = (size_t)t * a.ld_add + o;
     if (a.ydt == 2) {
@@ -275,27 +277,34 @@ __device__ __forceinline__ void add_slots(const ExpertsArgs& a, int o0, bool any
   }
 }
 
-template <typename T, bool I8, int WAVES, int FN, int D>
+// 16 FM outputs
+template <typename T, bool I8, int WAVES, int FM, int FN>
 __global__ __launch_bounds__(64 * WAVES) void experts_down_kernel(ExpertsArgs a, int mtile) {
   __shared__ int s_slot[EXPERTS_SLOTS];
-  __shared__ f32x4 s_sum[WAVES][FN][64];
+  __shared__ f32x4 s_sum[WAVES][FM * FN][64];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
-  const int unit = blockIdx.x / mtile, m = blockIdx.x - unit * mtile, m0 = m * 16;
+  const int unit = blockIdx.x / mtile, m = blockIdx.x - unit * mtile, m0 = m * 16 * FM;
   const int hit = *a.hit;
   int e;
   const int n = __builtin_amdgcn_readfirstlane(find_slots(a, unit, lane, wave, s_slot, &e));
   if (n == 0) {
-    if (hit == 0 && unit == 0) add_slots<WAVES>(a, m0, false);      // no slot at all
+    if (hit == 0 && unit == 0) add_slots<WAVES, 16 * FM>(a, m0, false);      // no slot at all
     return;
   }
   e = __builtin_amdgcn_readfirstlane(e);
   __syncthreads();
 
   constexpr int ES = I8 ? 1 : 2;
-  const char* const wb[1] = {reinterpret_cast<const char*>(a.w_down) + ((size_t)e * a.d + m0) * a.ff * ES};
+  const char* wb[FM];
+  int wn[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    wb[i] = reinterpret_cast<const char*>(a.w_down) + ((size_t)e * a.d + m0 + 16 * i) * a.ff * ES;
+    wn[i] = a.d - m0 - 16 * i;
+  }
   for (int c0 = 0; c0 < n; c0 += 16 * FN) {
     uint32_t xo[FN];
 #pragma unroll
@@ -303,73 +312,95 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_kernel(ExpertsArgs a,
       const int c = c0 + 16 * j + l16;
       xo[j] = c < n ? (uint32_t)s_slot[c] * (uint32_t)(a.ff * 2) : OOB;
     }
-    f32x4 acc[1][FN], sum[1];
-    part_of_product<T, I8, WAVES, 1, FN, D>(wb, a.d - m0, a.ff, reinterpret_cast<const char*>(a.h), xo, wave, lane, acc);
+    f32x4 acc[FM][FN];
+    part_of_product<T, I8, WAVES, FM, FN>(wb, wn, a.ff, reinterpret_cast<const char*>(a.h), xo, wave, lane, acc);
     if (c0 > 0) __syncthreads();
-    join_waves<WAVES, 1, FN>(acc, s_sum, wave, lane, sum);
-    const int c = c0 + 16 * wave + l16, o = m0 + 4 * lg;
-    if (wave >= FN || c >= n || o >= a.d) continue;
-    const int s = s_slot[c];
-    const float g = a.w[s];
-    if constexpr (I8) sum[0] *= scales4(a.s_down + (size_t)e * a.d, o, a.d);
-    *reinterpret_cast<f32x4*>(a.z + (size_t)s * a.d + o) = sum[0] * g;        // d % 8 == 0
+    put_parts<FM, FN>(acc, s_sum, wave, lane);
+    for (int f = wave; f < FM * FN; f += WAVES) {
+      const int c = c0 + 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
+      f32x4 sum = sum_parts<WAVES, FM * FN>(s_sum, f, lane);
+      if (c >= n || o >= a.d) continue;
+      const int s = s_slot[c];
+      const float g = a.w[s];
+      if constexpr (I8) sum *= scales4(a.s_down + (size_t)e * a.d, o, a.d);
+      float* z = a.z + (size_t)s * a.d + o;     // d % 8 == 0
+#pragma unroll
+      for (int v = 0; v < 4; ++v) __hip_atomic_store(z + v, sum[v] * g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
   }
-  // this workgroup's z before its count, the count before the others' z
-  __threadfence();
-  __syncthreads();
+  // z is written through to where every XCD sees it (stores of agent scope) and
+  // has arrived there before the count goes out; the last workgroup reads it
+  // from there.  (A release fence instead writes back an XCD's whole L2, for
+  // every workgroup: 32 tokens through 60 experts took 1595 us.)
+  wait_vm<0>();
+  bar_nofence();
   if (threadIdx.x == 0)
-    s_last = __hip_atomic_fetch_add(a.done + m, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == hit - 1;
+    s_last = __hip_atomic_fetch_add(a.done + m, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == hit - 1;
   __syncthreads();
   if (s_last == 0) return;
-  __threadfence();
-  add_slots<WAVES>(a, m0, true);
+  add_slots<WAVES, 16 * FM>(a, m0, true);
 }
 
-template <typename T, bool I8, int WAVES, int FN, int D>
+static int units_of(const ExpertsArgs& a) { return a.T * a.topk <= a.experts ? a.T * a.topk : a.experts; }
+
+template <typename T, bool I8, int WAVES, int P, int FN>
 static void go_up(const ExpertsArgs& a, hipStream_t s) {
-  const int mtile = (a.ff + 15) / 16, S = a.T * a.topk, units = S <= a.experts ? S : a.experts;
-  hipLaunchKernelGGL((experts_up_kernel<T, I8, WAVES, FN, D>), dim3((unsigned)(mtile * units + 1)), dim3(64 * WAVES), 0, s, a, mtile);
+  const int mtile = (a.ff + 16 * P - 1) / (16 * P);
+  hipLaunchKernelGGL((experts_up_kernel<T, I8, WAVES, P, FN>), dim3((unsigned)(mtile * units_of(a) + 1)),
+                     dim3(64 * WAVES), 0, s, a, mtile);
 }
-template <typename T, bool I8, int WAVES, int FN, int D>
+template <typename T, bool I8, int WAVES, int FM, int FN>
 static void go_down(const ExpertsArgs& a, hipStream_t s) {
-  const int mtile = experts_tiles(a.d), S = a.T * a.topk, units = S <= a.experts ? S : a.experts;
-  hipLaunchKernelGGL((experts_down_kernel<T, I8, WAVES, FN, D>), dim3((unsigned)(mtile * units)), dim3(64 * WAVES), 0, s, a, mtile);
+  const int mtile = (a.d + 16 * FM - 1) / (16 * FM);
+  hipLaunchKernelGGL((experts_down_kernel<T, I8, WAVES, FM, FN>), dim3((unsigned)(mtile * units_of(a))),
+                     dim3(64 * WAVES), 0, s, a, mtile);
 }
 
-// Waves of a workgroup: 8 where there are few workgroups and each wave still
-// has two runs of k, else 4.  Columns: 16 unless more slots of one expert are
-// likely; an expert with more of them goes over its weights again.
-template <typename T, bool I8, int FN, int D>
-static void go_waves(const ExpertsArgs& a, hipStream_t s) {
-  const int S = a.T * a.topk, units = S <= a.experts ? S : a.experts;
-  const int up = (a.ff + 15) / 16 * units, down = experts_tiles(a.d) * units;
-  const int run = 128 * D / (I8 ? 1 : 2);       // values of k in a run
-  if constexpr (FN < 4) {
-    if (up < 768 && a.d >= 16 * run) go_up<T, I8, 8, FN, D>(a, s);
-    else go_up<T, I8, 4, FN, D>(a, s);
-    if (down < 768 && a.ff >= 16 * run) go_down<T, I8, 8, FN, D>(a, s);
-    else go_down<T, I8, 4, FN, D>(a, s);
-  } else {
-    go_up<T, I8, 4, FN, D>(a, s);
-    go_down<T, I8, 4, FN, D>(a, s);
-  }
-}
-
+// A workgroup's outputs and waves, by what was measured (us of both kernels, bf16
+// weights; k in steps of 128 bytes):
+//   up    from 64 steps 16 outputs, 8 waves (8 experts of 4096 -> 14336, 8 tokens:
+//         428; 4 waves 445, 32 outputs 459); from 32 steps 32 outputs, 4 waves (8-bit,
+//         the same: 248; 16 outputs 254), 8 below 512 workgroups (one token through
+//         4 experts of 2048 -> 1408: 21; 4 waves 22); below 16 outputs, 4 waves (8-bit
+//         60 experts of 2048 -> 1408, 32 tokens: 115; 32 outputs 124)
+//   down  from 64 steps or below 512 workgroups 32 outputs, 8 waves (32 tokens
+//         through 8 experts of 14336 -> 4096: 487; 4 waves 490, 64 outputs 489); else 4
+//         waves and 16 outputs (64 experts of 1408 -> 2048, 64 tokens: 233; 32
+//         outputs 240) or, in 8 bits, 32 (32 tokens: 109; 16 outputs 116)
+// Columns: 16 up to 10 slots an expert on average (32 tokens through 2 of 8 experts:
+// 500, with 32 columns 516), 32 up to 24 (64 tokens: 654; with 16 702, with 64 712),
+// else 64 (128 tokens: 957; with 32 1007).  An expert with more slots goes over its
+// weights again.  The workgroups there: 32 outputs and 4 waves up, 64 and 8 (with 64
+// columns 4) down.
 template <typename T, bool I8>
-static void go_cols(const ExpertsArgs& a, hipStream_t s) {
-  const int S = a.T * a.topk;
-  if (a.T <= 16 || S <= 6 * a.experts) go_waves<T, I8, 1, 2>(a, s);
-  else if (a.T <= 32 || S <= 20 * a.experts) go_waves<T, I8, 2, I8 ? 1 : 2>(a, s);
-  else go_waves<T, I8, 4, 1>(a, s);
+static void go_layer(const ExpertsArgs& a, hipStream_t s) {
+  const int units = units_of(a), S = a.T * a.topk, ES = I8 ? 1 : 2;
+  const int up_steps = (a.d * ES + 127) / 128, down_steps = (a.ff * ES + 127) / 128;
+  if (a.T > 32 && S > 24 * a.experts) {
+    go_up<T, I8, 4, 2, 4>(a, s);
+    go_down<T, I8, 4, 4, 4>(a, s);
+    return;
+  }
+  if (a.T > 16 && S > 10 * a.experts) {
+    go_up<T, I8, 4, 2, 2>(a, s);
+    go_down<T, I8, 8, 4, 2>(a, s);
+    return;
+  }
+  if (up_steps >= 64) go_up<T, I8, 8, 1, 1>(a, s);
+  else if (up_steps < 32) go_up<T, I8, 4, 1, 1>(a, s);
+  else if (units * ((a.ff + 31) / 32) < 512) go_up<T, I8, 8, 2, 1>(a, s);
+  else go_up<T, I8, 4, 2, 1>(a, s);
+  if (down_steps >= 64 || units * ((a.d + 31) / 32) < 512) go_down<T, I8, 8, 2, 1>(a, s);
+  else go_down<T, I8, 4, I8 ? 2 : 1, 1>(a, s);
 }
 
 void launch_experts(const ExpertsArgs& a, int act, bool int8, hipStream_t s) {
   if (act == 0) {
-    if (int8) go_cols<half_t, true>(a, s);
-    else go_cols<half_t, false>(a, s);
+    if (int8) go_layer<half_t, true>(a, s);
+    else go_layer<half_t, false>(a, s);
   } else {
-    if (int8) go_cols<__bf16, true>(a, s);
-    else go_cols<__bf16, false>(a, s);
+    if (int8) go_layer<__bf16, true>(a, s);
+    else go_layer<__bf16, false>(a, s);
   }
 }
 

@@ -175,10 +175,14 @@ __device__ __forceinline__ bool locate_row_tile(const GroupArgs& a, int lane, in
 // (outputs past the last: 0), and of a row of x (-1: a row of zeros).
 __device__ __forceinline__ f32x4 output_scales(const GroupArgs& a, int g, int o) {
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  const float* p = a.ws + (size_t)g * a.d_out;
+  const float* p = a.ws + (size_t)g * a.d_out + o;
+  if (a.vec_scales) {
+    if (o < a.d_out) s = *reinterpret_cast<const f32x4*>(p);
+    return s;
+  }
 #pragma unroll
   for (int v = 0; v < 4; ++v)
-    if (o + v < a.d_out) s[v] = p[o + v];
+    if (o + v < a.d_out) s[v] = p[v];
   return s;
 }
 __device__ __forceinline__ float row_scale(const GroupArgs& a, int row) { return row >= 0 ? a.xs[row] : 0.f; }

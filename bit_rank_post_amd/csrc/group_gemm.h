@@ -28,6 +28,7 @@ struct GroupArgs {
   long ldx, ldy, ldo;            // row strides in elements
   int out_dtype;                 // 0 f16, 1 bf16, 2 f32
   int vec_out;                   // eight neighbouring outputs may be stored as 16-byte words
+  int vec_scales;                // I8: ws may be read as 16-byte words
   const float* xs;               // E4M3: [x_rows][ceil(d_in/128)] scales of x; I8: [x_rows]
   const float* ws;               // E4M3: [groups][ceil(d_out/128)][ceil(d_in/128)]; I8: [groups][d_out]
 };

@@ -658,6 +658,21 @@ static double tiles(const GroupArgs& a, GroupMode mode, int mt, int nt) {
 // groups, 77 .. 24434 rows and 256 .. 8000 inputs and outputs in f16 that the
 // constants were not taken from: the choice is the fastest or within 2 % for 36,
 // within 14 % for all.)
+// Products of 8-bit integers: a stage has the bytes and MFMAs of a 16-bit one and
+// twice its k, so starts and ends weigh twice as much.  With g the 256's (of 128 x
+// 32: 512's) of workgroups:
+//   rows kernels   L2 at 9.5 and 8 TB/s; the weights at 5.5 and 3.4 TB/s
+//   128 x 32       6 and 0.22 a stage, from 0.42 g on 0.53 g; at least half of that
+//                  and the weights at 5.7 TB/s
+//   128 x 128      8 and 0.45 + 0.25 g a stage up to g = 2, then 6.5 and 0.32 a stage
+//                  for each 256 more
+//   256 x 256      12 and 0.9 + 0.5 g a stage up to g = 1, then 8 and 1.55 a stage
+//                  for each 256
+// Both sides of some borders, us: 4096 -> 4096, one group of 64 rows: 32 x 32 rows
+// kernel 12, 128 x 32 13; 128 rows: 22, 13; 512 rows: 128 x 32 21, 128 x 128 26; 1024:
+// 41, 28; 2048: 128 x 128 41, 256 x 256 49; 4096: 76, 60; 2048 -> 1408, 64 ragged
+// groups of 24960 rows: 123, 125, even groups: 129, 104; 512 rows in 60 groups: 16 x 16
+// rows kernel 35, 32 x 32 48, 128 x 32 32.
 // Weight gradient, for each round of workgroups that run at once:
 //   128 x 128      8 and 1.36 a stage of 64 rows (512 workgroups)
 //   256 x 256      8 and 1.7 (256)
@@ -693,6 +708,22 @@ GroupPick choose_group(const GroupArgs& a, GroupMode mode, GroupType type) {
   const double weights = (double)(a.groups < a.rows ? a.groups : a.rows) * a.d_in * a.d_out * es;
   const auto least_of = [](double us, double memory) { return us > memory ? us : memory; };
   const double by_lds = weights / 4.6e6, direct = weights / 5.5e6;
+  if (type == GROUP_I8) {
+    const double g32 = tiles(a, mode, 128, 32) / 512, g = g128 / 256;
+    const double few = 10 + 0.95 * stages;        // 128 x 128 at g = 2
+    offer({false, ROWS_16x16, TILE_256x256},
+          least_of(r256 <= 1 ? 12 + stages * (0.9 + 0.5 * r256) : 8 + r256 * (8 + 1.55 * stages), by_lds + 8));
+    offer({false, ROWS_16x16, TILE_128x128},
+          least_of(g <= 2 ? 8 + g + stages * (0.45 + 0.25 * g) : few + (g - 2) * (6.5 + 0.32 * stages), by_lds + 4));
+    const double us32 = 6 + stages * (g32 <= 0.42 ? 0.22 : 0.53 * g32);
+    offer({false, ROWS_16x16, TILE_128x32}, least_of(us32, 0.8 * by_lds + 0.5 * us32));
+    const double avg = (double)a.rows / a.groups, row = a.d_in;
+    const double n16 = avg < 16 ? avg : 16, n32 = avg < 32 ? avg : 32;
+    offer({true, ROWS_16x16, TILE_256x256}, least_of(4 + tiles(a, mode, 16, 16) * (16 + n16) * row / 9.5e6, direct));
+    offer({true, ROWS_32x32, TILE_256x256},
+          least_of(4 + tiles(a, mode, 32, 32) * (32 + n32) * row / 8e6, weights / 3.4e6));
+    return best;
+  }
   if (mode == GROUP_DX) {
     offer({false, ROWS_16x16, TILE_256x256},
           least_of(r256 <= 1 ? 8 + stages * (1.25 + 0.4 * r256) : 8 * r256 + stages * 1.65 * (r256 + 0.25), by_lds + 8));

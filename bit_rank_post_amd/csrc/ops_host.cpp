@@ -463,6 +463,7 @@ tq_status tq_int8_gemm(const tq_group_desc* d, const int8_t* x, const float* x_s
   a.w = w;
   a.xs = x_scale;
   a.ws = w_scale;
+  a.vec_scales = d->d_out % 4 == 0 && aligned(w_scale, 16) ? 1 : 0;
   set_out(&a, y, a.ldy);
   return run_group(a, GROUP_Y, GROUP_I8, stream);
 }

@@ -12,8 +12,8 @@ CASES = [
     ((16, 16, 0), 7, 40, 912, 136), ((16, 16, 0), 70, 40, 912, 136),
     ((32, 32, 0), 4, 40, 912, 136), ((32, 32, 0), 70, 700, 912, 136),
     ((128, 32, 1), 30, 4200, 1040, 136), ((128, 32, 1), 70, 4200, 1040, 136),
-    ((128, 128, 1), 4, 9000, 912, 136), ((128, 128, 1), 70, 9000, 912, 136),
-    ((256, 256, 1), 16, 6000, 1040, 1032), ((256, 256, 1), 1, 4200, 912, 2056),
+    ((128, 128, 1), 4, 9000, 912, 520), ((128, 128, 1), 70, 9000, 912, 520),
+    ((256, 256, 1), 16, 9000, 1040, 1032), ((256, 256, 1), 66, 20000, 912, 1032), ((256, 256, 1), 1, 4200, 912, 4104),
 ]
 IDS = [f"{c[0][0]}x{c[0][1]}-{c[1]}g" for c in CASES]
 

@@ -10,9 +10,14 @@
 // gathering them from x.
 //
 // Bound by memory.  Sum: a thread takes 8 values of a token and requests them
-// from four slots at a time.  Gradient: a wave takes a slot, so that few
-// tokens still make many waves; the waves of one token follow each other and
-// find its dy in the cache.
+// from four slots at a time: 16384 tokens of two slots of 4096 values and an
+// addend, bf16: 98 us, 5.5 TB/s of what it must move (a large copy: 4.9); 32 tokens of
+// four of 2048: 3 us.  Gradient: of few tokens a wave takes a slot, so that they
+// still make many waves (1000 tokens of four slots of 2048: 10.4 us, a wave a
+// token 11.5; of eight of 4096: 33, 37), and the waves of one token find its dy in
+// the cache; from 4096 tokens a wave takes a token, keeps dy in registers and
+// requests the next slot's z ahead (4160 tokens of six of 2048: 51 us, 4.3 TB/s, a wave
+// a slot 55; 16384 of two of 4096: 137, 146).
 #include "layer_ops.h"
 #include "rows.h"
 
@@ -109,8 +114,72 @@ __global__ __launch_bounds__(256) void slot_sum_grad_kernel(SlotSumArgs a) {
   }
 }
 
+// A wave takes a token of up to 512 VPT values.
+template <typename Z, typename Y, int VPT>
+__global__ __launch_bounds__(256) void slot_sum_grad_tokens_kernel(SlotSumArgs a) {
+  const int lane = threadIdx.x & 63;
+  const long t = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.T) return;
+  Raw8<Y> u[VPT];
+  const Y* dy = reinterpret_cast<const Y*>(a.dy) + t * a.ld_dy;
+#pragma unroll
+  for (int q = 0; q < VPT; ++q)
+    if (q * 512 + lane * 8 < a.d) u[q].load(dy + q * 512 + lane * 8);
+  Raw8<Z> v[2][VPT];
+  int row[2];
+  auto request = [&](int j, int b) {
+    row[b] = j < a.topk ? slot_row(a, a.inv[t * a.topk + j]) : -1;
+    if (row[b] < 0 || a.dw == nullptr) return;
+    const Z* z = reinterpret_cast<const Z*>(a.z) + (long)row[b] * a.ldz;
+#pragma unroll
+    for (int q = 0; q < VPT; ++q)
+      if (q * 512 + lane * 8 < a.d) v[b][q].load(z + q * 512 + lane * 8);
+  };
+  auto slot = [&](int j, int b) {
+    const long s = t * a.topk + j;
+    float dot = 0.f;
+    if (row[b] >= 0) {
+      const float g = a.w == nullptr ? 1.f : a.w[s];
+      Z* dz = reinterpret_cast<Z*>(a.dz) + (long)row[b] * a.ld_dz;
+#pragma unroll
+      for (int q = 0; q < VPT; ++q) {
+        const int c = q * 512 + lane * 8;
+        if (c >= a.d) continue;
+        if (a.dw != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(u[q].get(e), v[b][q].get(e), dot);
+        }
+        if (a.dz != nullptr) {
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = g * u[q].get(e);
+          store8(dz + c, o);
+        }
+      }
+    }
+    if (a.dw != nullptr) {
+      dot = wave_sum(dot);
+      if (lane == 0) a.dw[s] = dot;
+    }
+  };
+  request(0, 0);
+  for (int j = 0; j < a.topk; j += 2) {
+    request(j + 1, 1);
+    slot(j, 0);
+    if (j + 1 >= a.topk) break;
+    request(j + 2, 0);
+    slot(j + 1, 1);
+  }
+}
+
 template <typename Z, typename Y>
 static void go_sum(const SlotSumArgs& a, bool grad, hipStream_t s) {
+  if (grad && a.T >= 4096 && a.d <= 4096) {
+    const dim3 grid((unsigned)(((long)a.T + 3) / 4));
+    if (a.d <= 2048) hipLaunchKernelGGL((slot_sum_grad_tokens_kernel<Z, Y, 4>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((slot_sum_grad_tokens_kernel<Z, Y, 8>), grid, dim3(256), 0, s, a);
+    return;
+  }
   if (grad) {
     const long slots = (long)a.T * a.topk, groups = (slots + 3) / 4;
     hipLaunchKernelGGL((slot_sum_grad_kernel<Z, Y>), dim3((unsigned)(groups < (1 << 20) ? groups : 1 << 20)), dim3(256), 0,

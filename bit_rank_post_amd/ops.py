@@ -489,8 +489,8 @@ def int8_gemm(x, x_scale, w, w_scale, y, off=None, src=None, src_div=1, stream=N
     _call(fn, dev, stream, ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y), ydt)
 
 
-def _swiglu_desc(fn, a, off, **mats):
-    """Descriptor of a [rows][2 ff] and matrices of ff or 2 ff columns."""
+def _gate_up(fn, a, off):
+    """Rows, ff and groups of a [rows][2 ff] and offsets; its type and stride."""
     adt, lda = _float(fn, a, "a"), _ld(fn, a, "a")
     rows, cols = a.shape
     if cols % 2:
@@ -502,22 +502,19 @@ def _swiglu_desc(fn, a, off, **mats):
             _refuse(fn, "off must be [groups + 1]")
         _int32(fn, off, "off", groups + 1)
     _fits(fn, rows, cols, groups)
-    d = SwigluDesc(rows, cols // 2, groups, adt, adt, _ptr(off), Rows(a.data_ptr(), lda), _ABSENT, _ABSENT, _ABSENT)
-    for name, (t, width, dtype) in mats.items():
-        setattr(d, name, _mat(fn, t, name, rows, cols // 2 * width, dtype))
-    return d
+    return rows, cols // 2, groups, adt, Rows(a.data_ptr(), lda)
 
 
 def swiglu(a, h, off=None, stream=None):
     """h = silu(gate) * up of a [rows][2 ff], the gate's ff columns first: h
     [rows][ff]; both float16, bfloat16 or float32.  off (int32 [groups + 1], as
-    of group_slots): only rows off[0] .. off[groups] - 1.  h may be a's first
-    half."""
+    of group_slots): only rows off[0] .. off[groups] - 1.  h may be a's first or
+    second half."""
     fn = "swiglu"
     dev = _device(fn, a, h, off)
     hdt = _float(fn, h, "h")
-    d = _swiglu_desc(fn, a, off, h=(h, 1, h.dtype))
-    d.h_dtype = hdt
+    rows, ff, groups, adt, ra = _gate_up(fn, a, off)
+    d = SwigluDesc(rows, ff, groups, adt, hdt, _ptr(off), ra, _mat(fn, h, "h", rows, ff, h.dtype))
     _call(fn, dev, stream, ctypes.byref(d))
 
 
@@ -526,8 +523,9 @@ def swiglu_int8(a, q, scale, off=None, stream=None):
     int8 [rows][ff], scale float32 [rows]."""
     fn = "swiglu_int8"
     dev = _device(fn, a, q, scale, off)
-    d = _swiglu_desc(fn, a, off)
-    _codes(fn, q, scale, (d.rows, d.ff))
+    rows, ff, groups, adt, ra = _gate_up(fn, a, off)
+    _codes(fn, q, scale, (rows, ff))
+    d = SwigluDesc(rows, ff, groups, adt, adt, _ptr(off), ra)
     _call(fn, dev, stream, ctypes.byref(d), _ptr(q), _ptr(scale))
 
 
@@ -538,8 +536,9 @@ def swiglu_grad(a, dh, da, h=None, off=None, stream=None):
     fn = "swiglu_grad"
     dev = _device(fn, a, dh, da, h, off)
     hdt = _float(fn, dh, "dh")
-    d = _swiglu_desc(fn, a, off, dh=(dh, 1, dh.dtype), da=(da, 2, a.dtype), h=(h, 1, a.dtype))
-    d.h_dtype = hdt
+    rows, ff, groups, adt, ra = _gate_up(fn, a, off)
+    d = SwigluDesc(rows, ff, groups, adt, hdt, _ptr(off), ra, _mat(fn, h, "h", rows, ff, a.dtype),
+                   _mat(fn, dh, "dh", rows, ff, dh.dtype), _mat(fn, da, "da", rows, 2 * ff, a.dtype))
     _call(fn, dev, stream, ctypes.byref(d))
 
 

@@ -41,6 +41,8 @@ def make(T, k, d, zdt, ydt, seed, extra=3, drop=True, wide=0):
     return rows, inv, z, w, add, dy, live, named
 
 
+# from 4096 tokens a wave takes a token of up to 2048 or 4096 values
+MANY = [(4097, 2, 136), (4100, 3, 2056), (4096, 1, 4104)]
 SIZES = [(1, 1, 8), (1, 8, 2048), (3, 2, 136), (32, 4, 2048), (130, 6, 1032), (700, 3, 4096), (5, 9, 5128), (2, 32, 16)]
 
 
@@ -65,7 +67,7 @@ def test_sum(T, k, d, zdt, ydt, kind):
     assert (y[:, d:] == -7).all()
 
 
-@pytest.mark.parametrize("T,k,d", SIZES)
+@pytest.mark.parametrize("T,k,d", SIZES + MANY)
 @pytest.mark.parametrize("zdt,ydt", [("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f16", "bf16")])
 @pytest.mark.parametrize("want", ["both", "dz", "dw", "plain"])
 def test_gradient(T, k, d, zdt, ydt, want):

@@ -10,10 +10,13 @@
 // NaN or an infinity gets a scale of NaN and codes of 0: all that it stands
 // for, and every product with it, reads NaN.
 //
-// Bound by memory.  swiglu and its gradient are streams of vectors of 8; a
-// row to be quantised is read once and stays in registers as f32 between the
-// maximum and the division: up to 4096 values (2048 of SwiGLU) in one wave,
-// which needs no barrier, above in a workgroup.
+// Bound by memory.  swiglu and its gradient are streams of vectors of 8: 32768 x
+// 14336 in bf16 497 us, 5.7 TB/s of what they must move (a large copy: 4.9), the
+// gradient of 24960 x 1408 with dh in f32 and h again 86 us, 5.7 TB/s.  A row to be
+// quantised is read once and stays in registers as f32 between the maximum and
+// the division: below 2048 values in one wave, which needs no barrier, above in
+// a workgroup; above 32768 the rest is read again (24960 x 1408, of SwiGLU in f16:
+// 41 us, 4.3 TB/s).
 #include "layer_ops.h"
 #include "rows.h"
 
@@ -260,15 +263,23 @@ void launch_swiglu(const SwigluArgs& a, int adt, int hdt, hipStream_t s) { go_sw
 void launch_swiglu_grad(const SwigluArgs& a, int adt, int hdt, hipStream_t s) { go_swiglu_a(a, true, adt, hdt, s); }
 
 template <class Rows>
-static void go_int8(const Int8RowsArgs& a, Rows x, bool swiglu, hipStream_t s) {
+static void go_int8(const Int8RowsArgs& a, Rows x, hipStream_t s) {
   const int nv = a.d / 8;
   const long most = 1 << 16;                    // workgroups; more rows are taken in turns
   const unsigned by_wave = (unsigned)(((long)a.rows + 3) / 4 < most ? ((long)a.rows + 3) / 4 : most);
   const unsigned by_group = (unsigned)(a.rows < most ? a.rows : most);
-  if (nv <= 128) hipLaunchKernelGGL((int8_rows_kernel<Rows, true, 2>), dim3(by_wave), dim3(256), 0, s, x, a);
-  else if (nv <= 256) hipLaunchKernelGGL((int8_rows_kernel<Rows, true, 4>), dim3(by_wave), dim3(256), 0, s, x, a);
-  else if (nv <= 512 && !swiglu) hipLaunchKernelGGL((int8_rows_kernel<Rows, true, 8>), dim3(by_wave), dim3(256), 0, s, x, a);
-  else {
+  // us for 64, 4096 and 16384 rows of bf16, a wave and a workgroup (two vectors a
+  // thread) a row: 1024 values 2.9, 3.9, 10.9 and 3.1, 4.6, 11.1; 1408: 3.3, 4.6, 14.8
+  // and 3.1, 5.6, 14.8; 2048: 3.6, 5.4, 18.9 and 3.2, 6.1, 17.9; 4096: 4.8, 10.5, 35.6 and
+  // 3.3, 11.2, 31.6.  Two and four vectors a thread: 8192 values 3.4, 17.8, 70.7 and
+  // 3.9, 19.2, 76.1; 14336 values, 64 and 4096 rows: 4.2, 38.0 and 4.1, 32.3.
+  if (nv <= 128) {
+    hipLaunchKernelGGL((int8_rows_kernel<Rows, true, 2>), dim3(by_wave), dim3(256), 0, s, x, a);
+  } else if (nv < 256) {
+    hipLaunchKernelGGL((int8_rows_kernel<Rows, true, 4>), dim3(by_wave), dim3(256), 0, s, x, a);
+  } else if (nv <= 1024) {
+    hipLaunchKernelGGL((int8_rows_kernel<Rows, false, 2>), dim3(by_group), dim3((nv + 127) / 128 * 64), 0, s, x, a);
+  } else {
     const int waves = (nv + 255) / 256 < 16 ? (nv + 255) / 256 : 16;
     hipLaunchKernelGGL((int8_rows_kernel<Rows, false, 4>), dim3(by_group), dim3(64 * waves), 0, s, x, a);
   }
@@ -276,8 +287,8 @@ static void go_int8(const Int8RowsArgs& a, Rows x, bool swiglu, hipStream_t s) {
 template <typename T>
 static void go_int8_t(const Int8RowsArgs& a, bool swiglu, hipStream_t s) {
   const T* p = reinterpret_cast<const T*>(a.x);
-  if (swiglu) go_int8(a, SwigluRows<T>{p, a.ldx}, true, s);
-  else go_int8(a, PlainRows<T>{p, a.ldx}, false, s);
+  if (swiglu) go_int8(a, SwigluRows<T>{p, a.ldx}, s);
+  else go_int8(a, PlainRows<T>{p, a.ldx}, s);
 }
 void launch_int8_rows(const Int8RowsArgs& a, int xdt, bool swiglu, hipStream_t s) {
   if (xdt == 0) go_int8_t<half_t>(a, swiglu, s);

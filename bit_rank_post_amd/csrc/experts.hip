@@ -18,7 +18,12 @@
 // z and counts itself done for its 16 outputs; the last one adds the slots of
 // each token in order.  So the sum has one order whichever workgroup is last,
 // and there is no third launch and no atomic on y.  The up kernel sets the
-// counters to zero.
+// counters to zero.  A single token's down workgroups go over all its slots
+// instead.
+//
+// 32 tokens through four of 60 experts of 2048 -> 1408, f16: 171 us, 5.4 TB/s of the
+// 53 experts' weights (a plain read of a larger buffer: 5.5); one token through two
+// of eight of 4096 -> 14336 in 8 bits: 71 us, 5.0 TB/s.
 //
 // 8-bit weights (integers with an f32 scale for each output) are unpacked to
 // the activations' type, exactly, next to the MFMA; the scale meets the sum.
@@ -103,72 +108,80 @@ __device__ __forceinline__ f32x4 sum_parts(const f32x4 (*s_sum)[F][64], int f, i
   return v;
 }
 
-// FM fragments of 16 rows of a matrix [..][K] (their bases in wb, of fragment i
-// rows up to wn[i] exist) times 16 FN columns, whose rows of 16-bit values start xo bytes
-// into xb (OOB: zeros).  The waves share k; acc holds this wave's part.
-template <typename T, bool I8, int WAVES, int FM, int FN>
-__device__ __forceinline__ void part_of_product(const char* const (&wb)[FM], const int (&wn)[FM], int K, const char* xb,
-                                                const uint32_t (&xo)[FN], int wave, int lane, f32x4 (&acc)[FM][FN]) {
-  constexpr int ES = I8 ? 1 : 2, XB = I8 ? 2 : 1;   // bytes of a weight; 16-byte loads of x for one of W
-  const int l16 = lane & 15, lg = lane >> 4;
-  const int bytes = K * ES, nstep = (bytes + 127) >> 7;
-  __amdgpu_buffer_rsrc_t rw[FM];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) rw[i] = make_rsrc(wb[i], (uint32_t)OOB);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xb, (uint32_t)OOB);
-  uint32_t vw[FM];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) vw[i] = l16 < wn[i] ? (uint32_t)l16 * (uint32_t)bytes + lg * 16u : OOB;
-  struct Step {
-    u32x4 w[FM][2], x[FN][2][XB];
-  };
-  auto fetch = [&](int st, Step& r) {
+// A step of k: 128 bytes of each of 16 FM weight rows, and what they meet of 16 FN
+// columns of 16-bit values.
+template <typename T, bool I8, int FM, int FN> struct Step {
+  static constexpr int XB = I8 ? 2 : 1;         // 16-byte loads of a column for one of a weight row
+  u32x4 w[FM][2], x[FN][2][XB];
+
+  // step st of rows of `bytes` bytes: vw, xo are byte offsets of this lane's row
+  // and column (OOB: zeros)
+  __device__ __forceinline__ void fetch(int st, int bytes, int lg, const __amdgpu_buffer_rsrc_t (&rw)[FM],
+                                        const uint32_t (&vw)[FM], __amdgpu_buffer_rsrc_t rx, const uint32_t (&xo)[FN]) {
     const uint32_t so = st * 128u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // bytes 64 h + 16 lg of the step's 128: past the row, nothing is read
       const bool ok = st * 128 + h * 64 + lg * 16 < bytes;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) r.w[i][h] = bload128(rw[i], ok ? vw[i] + h * 64u : OOB, so);
+      for (int i = 0; i < FM; ++i) w[i][h] = bload128(rw[i], ok ? vw[i] + h * 64u : OOB, so);
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int q = 0; q < XB; ++q)
-          r.x[j][h][q] = bload128(rx, ok && xo[j] != OOB ? xo[j] + (h * 64u + lg * 16u) * XB + q * 16u : OOB, so * XB);
+          x[j][h][q] = bload128(rx, ok && xo[j] != OOB ? xo[j] + (h * 64u + lg * 16u) * XB + q * 16u : OOB, so * XB);
     }
-  };
-  auto multiply = [&](const Step& r) {
+  }
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[FM][FN]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         if constexpr (I8) {
           u32x4 w0, w1;
-          Unpack8<T>::get(r.w[i][h], w0, w1);
+          Unpack8<T>::get(w[i][h], w0, w1);
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
-            acc[i][j] = mfma_half<T>(w0, r.x[j][h][0], acc[i][j]);
-            acc[i][j] = mfma_half<T>(w1, r.x[j][h][1], acc[i][j]);
+            acc[i][j] = mfma_half<T>(w0, x[j][h][0], acc[i][j]);
+            acc[i][j] = mfma_half<T>(w1, x[j][h][1], acc[i][j]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = mfma_half<T>(r.w[i][h], r.x[j][h][0], acc[i][j]);
+          for (int j = 0; j < FN; ++j) acc[i][j] = mfma_half<T>(w[i][h], x[j][h][0], acc[i][j]);
         }
       }
-  };
+  }
+};
+
+// FM fragments of 16 rows of a matrix [..][K] (their bases in wb, of fragment i
+// rows up to wn[i] exist) times 16 FN columns, whose rows of 16-bit values start xo
+// bytes into xb (OOB: zeros).  The waves share k; acc holds this wave's part.
+template <typename T, bool I8, int WAVES, int FM, int FN>
+__device__ __forceinline__ void part_of_product(const char* const (&wb)[FM], const int (&wn)[FM], int K, const char* xb,
+                                                const uint32_t (&xo)[FN], int wave, int lane, f32x4 (&acc)[FM][FN]) {
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int bytes = K * (I8 ? 1 : 2), nstep = (bytes + 127) >> 7;
+  __amdgpu_buffer_rsrc_t rw[FM];
+  uint32_t vw[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    rw[i] = make_rsrc(wb[i], (uint32_t)OOB);
+    vw[i] = l16 < wn[i] ? (uint32_t)l16 * (uint32_t)bytes + lg * 16u : OOB;
+  }
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xb, (uint32_t)OOB);
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Step r0, r1;
+  Step<T, I8, FM, FN> r0, r1;
   int st = wave;
-  if (st < nstep) fetch(st, r0);
+  if (st < nstep) r0.fetch(st, bytes, lg, rw, vw, rx, xo);
   for (; st < nstep; st += 2 * WAVES) {
-    if (st + WAVES < nstep) fetch(st + WAVES, r1);
-    multiply(r0);
+    if (st + WAVES < nstep) r1.fetch(st + WAVES, bytes, lg, rw, vw, rx, xo);
+    r0.multiply(acc);
     if (st + WAVES >= nstep) break;
-    if (st + 2 * WAVES < nstep) fetch(st + 2 * WAVES, r0);
-    multiply(r1);
+    if (st + 2 * WAVES < nstep) r0.fetch(st + 2 * WAVES, bytes, lg, rw, vw, rx, xo);
+    r1.multiply(acc);
   }
 }
 
@@ -181,15 +194,16 @@ __device__ __forceinline__ f32x4 scales4(const float* p, int o, int n) {
   return s;
 }
 
-// 16 P outputs of the gate and the same of the up matrix
-template <typename T, bool I8, int WAVES, int P, int FN>
+// 16 P outputs of the gate and the same of the up matrix.  ONE: a single token,
+// whose slots are the work units as they are.
+template <typename T, bool I8, int WAVES, int P, int FN, bool ONE>
 __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, int mtile) {
   __shared__ int s_slot[EXPERTS_SLOTS];
   __shared__ f32x4 s_sum[WAVES][2 * P * FN][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
-  if (blockIdx.x == gridDim.x - 1) {
+  if (!ONE && blockIdx.x == gridDim.x - 1) {
     // one workgroup more: clears the counters, counts the experts with a slot
     for (int i = threadIdx.x; i < experts_tiles(a.d); i += 64 * WAVES) a.done[i] = 0;
     int* s_hit = s_slot;                        // [1024 / 32]
@@ -207,11 +221,16 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
     return;
   }
   const int unit = blockIdx.x / mtile, m0 = (blockIdx.x - unit * mtile) * 16 * P;
-  int e;
-  const int n = __builtin_amdgcn_readfirstlane(find_slots(a, unit, lane, wave, s_slot, &e));
-  if (n == 0) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  __syncthreads();
+  int e, n = 1;
+  if constexpr (ONE) {
+    e = a.ids[unit];
+    if (e < 0 || e >= a.experts) return;
+  } else {
+    n = __builtin_amdgcn_readfirstlane(find_slots(a, unit, lane, wave, s_slot, &e));
+    if (n == 0) return;
+    e = __builtin_amdgcn_readfirstlane(e);
+    __syncthreads();
+  }
 
   constexpr int ES = I8 ? 1 : 2;
   const char* w = reinterpret_cast<const char*>(a.w_up) + ((size_t)e * 2 * a.ff + m0) * a.d * ES;
@@ -228,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int c = c0 + 16 * j + l16;
-      xo[j] = c < n ? (uint32_t)(s_slot[c] / a.topk) * (uint32_t)(a.ldx * 2) : OOB;
+      xo[j] = c < n ? (ONE ? 0u : (uint32_t)(s_slot[c] / a.topk) * (uint32_t)(a.ldx * 2)) : OOB;
     }
     f32x4 acc[2 * P][FN];
     part_of_product<T, I8, WAVES, 2 * P, FN>(wb, wn, a.d, reinterpret_cast<const char*>(a.x), xo, wave, lane, acc);
@@ -246,8 +265,24 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
       T4 h;
 #pragma unroll
       for (int v = 0; v < 4; ++v) h[v] = (T)(silu_f(g[v]) * u[v]);
-      *reinterpret_cast<T4*>(reinterpret_cast<T*>(a.h) + (size_t)s_slot[c] * a.ff + o) = h;   // ff % 8 == 0
+      const int s = ONE ? unit : s_slot[c];
+      *reinterpret_cast<T4*>(reinterpret_cast<T*>(a.h) + (size_t)s * a.ff + o) = h;       // ff % 8 == 0
     }
+  }
+}
+
+// y[t][o] = add[t][o] + v
+__device__ __forceinline__ void put_y(const ExpertsArgs& a, int t, int o, float v) {
+  const size_t at = (size_t)t * a.ldy + o, from = (size_t)t * a.ld_add + o;
+  if (a.ydt == 2) {
+    if (a.add != nullptr) v += reinterpret_cast<const float*>(a.add)[from];
+    reinterpret_cast<float*>(a.y)[at] = v;
+  } else if (a.ydt == 1) {
+    if (a.add != nullptr) v += (float)reinterpret_cast<const __bf16*>(a.add)[from];
+    reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)v;
+  } else {
+    if (a.add != nullptr) v += (float)reinterpret_cast<const half_t*>(a.add)[from];
+    reinterpret_cast<half_t*>(a.y)[at] = (half_t)v;
   }
 }
 
@@ -263,17 +298,7 @@ __device__ __forceinline__ void add_slots(const ExpertsArgs& a, int o0, bool any
         const int s = t * a.topk + j, e = a.ids[s];
         if (e >= 0 && e < a.experts) y += __hip_atomic_load(a.z + (size_t)s * a.d + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-    const size_t at = (size_t)t * a.ldy + o, from = (size_t)t * a.ld_add + o;
-    if (a.ydt == 2) {
-      if (a.add != nullptr) y += reinterpret_cast<const float*>(a.add)[from];
-      reinterpret_cast<float*>(a.y)[at] = y;
-    } else if (a.ydt == 1) {
-      if (a.add != nullptr) y += (float)reinterpret_cast<const __bf16*>(a.add)[from];
-      reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)y;
-    } else {
-      if (a.add != nullptr) y += (float)reinterpret_cast<const half_t*>(a.add)[from];
-      reinterpret_cast<half_t*>(a.y)[at] = (half_t)y;
-    }
+    put_y(a, t, o, y);
   }
 }
 
@@ -341,13 +366,65 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_kernel(ExpertsArgs a,
   add_slots<WAVES, 16 * FM>(a, m0, true);
 }
 
+// The down product of a single token: 16 outputs over all of its slots, one after
+// the other in one run of steps, so that no workgroup waits for another's sums.
+template <typename T, bool I8, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void experts_down_one_kernel(ExpertsArgs a) {
+  __shared__ f32x4 s_sum[WAVES][1][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lg = lane >> 4, m0 = blockIdx.x * 16, o = m0 + 4 * lg;
+  const int bytes = a.ff * (I8 ? 1 : 2), nstep = (bytes + 127) >> 7, total = nstep * a.topk;
+  const uint32_t row = l16 < a.d - m0 ? (uint32_t)l16 * (uint32_t)bytes + lg * 16u : OOB;
+  // (slot, step of its k) of a step of the run; an id outside reads zeros
+  auto fetch = [&](int st, int j, Step<T, I8, 1, 1>& r) {
+    const int e = sload(a.ids, j);
+    const bool live = e >= 0 && e < a.experts;
+    const __amdgpu_buffer_rsrc_t rw[1] = {make_rsrc(
+        reinterpret_cast<const char*>(a.w_down) + ((size_t)(live ? e : 0) * a.d + m0) * bytes, (uint32_t)OOB)};
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(reinterpret_cast<const char*>(a.h) + (size_t)j * a.ff * 2, (uint32_t)OOB);
+    const uint32_t vw[1] = {live ? row : OOB}, xo[1] = {live && l16 == 0 ? 0u : OOB};
+    r.fetch(st - j * nstep, bytes, lg, rw, vw, rx, xo);
+  };
+  f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}}, sum[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+  // a slot's part of this wave, times its weight and scales
+  auto close = [&](int j) {
+    const int e = sload(a.ids, j);
+    if (e >= 0 && e < a.experts) {
+      f32x4 v = acc[0][0];
+      if constexpr (I8) v *= scales4(a.s_down + (size_t)e * a.d, o, a.d);
+      sum[0][0] += v * a.w[j];
+    }
+    acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  Step<T, I8, 1, 1> r0, r1;
+  int st = wave, j0 = wave / nstep, j1 = 0, at = j0;      // slots of r0, of r1 and of acc
+  if (st < total) fetch(st, j0, r0);
+  for (; st < total; st += 2 * WAVES) {
+    if (st + WAVES < total) fetch(st + WAVES, j1 = (st + WAVES) / nstep, r1);
+    if (j0 != at) close(at), at = j0;
+    r0.multiply(acc);
+    if (st + WAVES >= total) break;
+    if (st + 2 * WAVES < total) fetch(st + 2 * WAVES, j0 = (st + 2 * WAVES) / nstep, r0);
+    if (j1 != at) close(at), at = j1;
+    r1.multiply(acc);
+  }
+  if (wave < total) close(at);
+  put_parts<1, 1>(sum, s_sum, wave, lane);
+  if (wave > 0 || l16 > 0) return;
+  const f32x4 y = sum_parts<WAVES, 1>(s_sum, 0, lane);
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (o + v < a.d) put_y(a, 0, o + v, y[v]);
+}
+
 static int units_of(const ExpertsArgs& a) { return a.T * a.topk <= a.experts ? a.T * a.topk : a.experts; }
 
-template <typename T, bool I8, int WAVES, int P, int FN>
+template <typename T, bool I8, int WAVES, int P, int FN, bool ONE = false>
 static void go_up(const ExpertsArgs& a, hipStream_t s) {
   const int mtile = (a.ff + 16 * P - 1) / (16 * P);
-  hipLaunchKernelGGL((experts_up_kernel<T, I8, WAVES, P, FN>), dim3((unsigned)(mtile * units_of(a) + 1)),
-                     dim3(64 * WAVES), 0, s, a, mtile);
+  hipLaunchKernelGGL((experts_up_kernel<T, I8, WAVES, P, FN, ONE>),
+                     dim3((unsigned)(ONE ? mtile * a.topk : mtile * units_of(a) + 1)), dim3(64 * WAVES), 0, s, a, mtile);
 }
 template <typename T, bool I8, int WAVES, int FM, int FN>
 static void go_down(const ExpertsArgs& a, hipStream_t s) {
@@ -358,11 +435,16 @@ static void go_down(const ExpertsArgs& a, hipStream_t s) {
 
 // A workgroup's outputs and waves, by what was measured (us of both kernels, bf16
 // weights; k in steps of 128 bytes):
+//   one   a single token: no slots to look for, and the down kernel takes 16 outputs
+//         of all its slots (8-bit, 4 of 60 experts of 2048 -> 1408: 16, by the kernels
+//         below 17; 8 of 16 of 5120 -> 1536: 49, 61; one of 32 of 4096 -> 4096 in 16 bits:
+//         25, 30).  Up 8 waves from 32 steps (8 of 64 of 2048 -> 1024: 28; 4 waves 29),
+//         else 4 (8-bit, 60 experts: 15.7; 8 waves 15.9); down 8 waves from 256 workgroups
+//         (5120: 50; 16 waves 53), else 16 (2048: 15.7; 8 waves 16.3)
 //   up    from 64 steps 16 outputs, 8 waves (8 experts of 4096 -> 14336, 8 tokens:
 //         428; 4 waves 445, 32 outputs 459); from 32 steps 32 outputs, 4 waves (8-bit,
-//         the same: 248; 16 outputs 254), 8 below 512 workgroups (one token through
-//         4 experts of 2048 -> 1408: 21; 4 waves 22); below 16 outputs, 4 waves (8-bit
-//         60 experts of 2048 -> 1408, 32 tokens: 115; 32 outputs 124)
+//         the same: 248; 16 outputs 254), 8 below 512 workgroups; below 16 outputs, 4
+//         waves (8-bit 60 experts of 2048 -> 1408, 32 tokens: 115; 32 outputs 124)
 //   down  from 64 steps or below 512 workgroups 32 outputs, 8 waves (32 tokens
 //         through 8 experts of 14336 -> 4096: 487; 4 waves 490, 64 outputs 489); else 4
 //         waves and 16 outputs (64 experts of 1408 -> 2048, 64 tokens: 233; 32
@@ -376,6 +458,14 @@ template <typename T, bool I8>
 static void go_layer(const ExpertsArgs& a, hipStream_t s) {
   const int units = units_of(a), S = a.T * a.topk, ES = I8 ? 1 : 2;
   const int up_steps = (a.d * ES + 127) / 128, down_steps = (a.ff * ES + 127) / 128;
+  if (a.T == 1) {
+    if (up_steps >= 32) go_up<T, I8, 8, 1, 1, true>(a, s);
+    else go_up<T, I8, 4, 1, 1, true>(a, s);
+    const int n = experts_tiles(a.d);
+    if (n >= 256) hipLaunchKernelGGL((experts_down_one_kernel<T, I8, 8>), dim3((unsigned)n), dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((experts_down_one_kernel<T, I8, 16>), dim3((unsigned)n), dim3(1024), 0, s, a);
+    return;
+  }
   if (a.T > 32 && S > 24 * a.experts) {
     go_up<T, I8, 4, 2, 4>(a, s);
     go_down<T, I8, 4, 4, 4>(a, s);

@@ -94,7 +94,7 @@ def run(m, ydt="f32", add=None, T=None, ws=None, **kw):
 SIZES = [(8, 1, 1, 64, 48), (8, 1, 2, 256, 96), (60, 1, 4, 256, 136), (60, 5, 4, 520, 264), (60, 32, 4, 256, 96),
          (8, 16, 2, 136, 72), (8, 17, 2, 256, 136), (8, 40, 2, 136, 264), (3, 64, 2, 264, 72), (1, 33, 1, 64, 40),
          (1, 100, 1, 128, 64), (2, 512, 2, 64, 32), (128, 3, 8, 72, 24), (1024, 2, 32, 16, 16), (300, 128, 8, 32, 16),
-         (4, 2, 2, 4096, 2056), (2, 1, 1, 1032, 5000)]
+         (4, 2, 2, 4096, 2056), (2, 1, 1, 1032, 5000), (5, 1, 3, 4104, 200), (40, 1, 32, 48, 24), (6, 1, 2, 2048, 1032)]
 
 
 @pytest.mark.parametrize("E,T,k,d,ff", SIZES)
@@ -113,7 +113,8 @@ def test_layer(E, T, k, d, ff, dtype, int8):
         assert torch.equal(run(m, ydt), y.to(DT[ydt]))
 
 
-@pytest.mark.parametrize("E,T,k,d,ff", [(8, 6, 3, 128, 80), (2, 30, 2, 128, 80), (40, 4, 4, 128, 80), (1, 20, 4, 64, 48)])
+@pytest.mark.parametrize("E,T,k,d,ff", [(8, 6, 3, 128, 80), (2, 30, 2, 128, 80), (40, 4, 4, 128, 80), (1, 20, 4, 64, 48),
+                                        (3, 1, 8, 128, 80), (12, 1, 5, 4112, 336)])
 @pytest.mark.parametrize("int8", [False, True])
 def test_an_expert_named_twice_and_ids_outside(E, T, k, d, ff, int8):
     for repeat, bad in ((True, False), (False, True), (True, True)):
@@ -129,7 +130,7 @@ def test_an_expert_named_twice_and_ids_outside(E, T, k, d, ff, int8):
         check("y", y, ref, 1.01 * tol + 2 * half_step(ref, torch.float32) + 2.0 ** -24 * add.double().abs())
 
 
-@pytest.mark.parametrize("E,T", [(8, 2), (2, 30)])
+@pytest.mark.parametrize("E,T", [(8, 1), (8, 2), (2, 30)])
 def test_no_slot_counts(E, T):
     m = make(E, T, 2, 64, 48, "f16", False, 4)
     m[1][:] = torch.tensor([-1, E], dtype=I32)

@@ -153,35 +153,60 @@ template <typename T, bool I8, int FM, int FN> struct Step {
   }
 };
 
-// FM fragments of 16 rows of a matrix [..][K] (their bases in wb, of fragment i
-// rows up to wn[i] exist) times 16 FN columns, whose rows of 16-bit values start xo
-// bytes into xb (OOB: zeros).  The waves share k; acc holds this wave's part.
-template <typename T, bool I8, int WAVES, int FM, int FN>
-__device__ __forceinline__ void part_of_product(const char* const (&wb)[FM], const int (&wn)[FM], int K, const char* xb,
-                                                const uint32_t (&xo)[FN], int wave, int lane, f32x4 (&acc)[FM][FN]) {
-  const int l16 = lane & 15, lg = lane >> 4;
-  const int bytes = K * (I8 ? 1 : 2), nstep = (bytes + 127) >> 7;
-  __amdgpu_buffer_rsrc_t rw[FM];
-  uint32_t vw[FM];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    rw[i] = make_rsrc(wb[i], (uint32_t)OOB);
-    vw[i] = l16 < wn[i] ? (uint32_t)l16 * (uint32_t)bytes + lg * 16u : OOB;
-  }
+// FM fragments of 16 weight rows of K values times 16 FN columns of 16-bit values,
+// for `tiles` such products one after the other.  The waves share k in
+// interleaved steps; a wave requests its next step, of the next product too,
+// before it multiplies the last.  (The last request of a run is not made, so the
+// compiler's waits for a step cover its successor too: more requests in flight are
+// no gain here, they were 3 to 8 % slower with 16-bit weights.)  tile(t, rw, vw,
+// xo) sets what Step::fetch takes; done(t, acc) gets this wave's part; all waves
+// call it for all tiles.
+template <typename T, bool I8, int WAVES, int FM, int FN, class Tile, class Done>
+__device__ __forceinline__ void stream_tiles(int tiles, int K, const char* xb, int wave, int lane, Tile tile, Done done) {
+  const int lg = lane >> 4;
+  const int bytes = K * (I8 ? 1 : 2), nstep = (bytes + 127) >> 7, per = (nstep + WAVES - 1) / WAVES;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(xb, (uint32_t)OOB);
+  __amdgpu_buffer_rsrc_t rw[FM];
+  uint32_t vw[FM], xo[FN];
+  int ft = -1, fi = per;                        // tile and step that were requested last
+  auto request = [&](Step<T, I8, FM, FN>& r) {
+    if (fi == per) {
+      fi = 0;
+      if (++ft < tiles) tile(ft, rw, vw, xo);
+    }
+    if (ft >= tiles) return;
+    // (a step past the last one reads nothing)
+    r.fetch(wave + WAVES * fi, bytes, lg, rw, vw, rx, xo);
+    ++fi;
+  };
+  f32x4 acc[FM][FN];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
   Step<T, I8, FM, FN> r0, r1;
-  int st = wave;
-  if (st < nstep) r0.fetch(st, bytes, lg, rw, vw, rx, xo);
-  for (; st < nstep; st += 2 * WAVES) {
-    if (st + WAVES < nstep) r1.fetch(st + WAVES, bytes, lg, rw, vw, rx, xo);
+  int t = 0, i = 0;
+  request(r0);
+  for (;;) {
+    request(r1);
     r0.multiply(acc);
-    if (st + WAVES >= nstep) break;
-    if (st + 2 * WAVES < nstep) r0.fetch(st + 2 * WAVES, bytes, lg, rw, vw, rx, xo);
+    if (++i == per) {
+      done(t, acc);
+      if (++t == tiles) break;
+      clear();
+      i = 0;
+    }
+    request(r0);
     r1.multiply(acc);
+    if (++i == per) {
+      done(t, acc);
+      if (++t == tiles) break;
+      clear();
+      i = 0;
+    }
   }
 }
 
@@ -198,8 +223,8 @@ __device__ __forceinline__ f32x4 scales4(const float* p, int o, int n) {
 // whose slots are the work units as they are.
 template <typename T, bool I8, int WAVES, int P, int FN, bool ONE>
 __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, int mtile) {
-  __shared__ int s_slot[EXPERTS_SLOTS];
-  __shared__ f32x4 s_sum[WAVES][2 * P * FN][64];
+  __shared__ int s_slot[ONE ? 1 : EXPERTS_SLOTS];
+  __shared__ f32x4 s_sum[ONE ? 1 : 2][WAVES][2 * P * FN][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
@@ -231,44 +256,47 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_kernel(ExpertsArgs a, i
     e = __builtin_amdgcn_readfirstlane(e);
     __syncthreads();
   }
-
   constexpr int ES = I8 ? 1 : 2;
-  const char* w = reinterpret_cast<const char*>(a.w_up) + ((size_t)e * 2 * a.ff + m0) * a.d * ES;
-  const char* wb[2 * P];
-  int wn[2 * P];
+  const int chunks = ONE ? 1 : (n + 16 * FN - 1) / (16 * FN);
+  const char* const w0 = reinterpret_cast<const char*>(a.w_up) + (size_t)e * 2 * a.ff * a.d * ES;
+  stream_tiles<T, I8, WAVES, 2 * P, FN>(
+      chunks, a.d, reinterpret_cast<const char*>(a.x), wave, lane,
+      [&](int t, __amdgpu_buffer_rsrc_t (&rw)[2 * P], uint32_t (&vw)[2 * P], uint32_t (&xo)[FN]) {
+        const int c0 = t * 16 * FN;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    wb[p] = w + (size_t)16 * p * a.d * ES;
-    wb[P + p] = wb[p] + (size_t)a.ff * a.d * ES;
-    wn[p] = wn[P + p] = a.ff - m0 - 16 * p;
-  }
-  for (int c0 = 0; c0 < n; c0 += 16 * FN) {
-    uint32_t xo[FN];
+        for (int p = 0; p < P; ++p) {
+          const char* w = w0 + (size_t)(m0 + 16 * p) * a.d * ES;
+          rw[p] = make_rsrc(w, (uint32_t)OOB);
+          rw[P + p] = make_rsrc(w + (size_t)a.ff * a.d * ES, (uint32_t)OOB);
+          vw[p] = vw[P + p] = l16 < a.ff - m0 - 16 * p ? (uint32_t)l16 * (uint32_t)(a.d * ES) + lg * 16u : OOB;
+        }
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int c = c0 + 16 * j + l16;
-      xo[j] = c < n ? (ONE ? 0u : (uint32_t)(s_slot[c] / a.topk) * (uint32_t)(a.ldx * 2)) : OOB;
-    }
-    f32x4 acc[2 * P][FN];
-    part_of_product<T, I8, WAVES, 2 * P, FN>(wb, wn, a.d, reinterpret_cast<const char*>(a.x), xo, wave, lane, acc);
-    if (c0 > 0) __syncthreads();
-    put_parts<2 * P, FN>(acc, s_sum, wave, lane);
-    for (int f = wave; f < P * FN; f += WAVES) {
-      const int c = c0 + 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
-      f32x4 g = sum_parts<WAVES, 2 * P * FN>(s_sum, f, lane), u = sum_parts<WAVES, 2 * P * FN>(s_sum, P * FN + f, lane);
-      if (c >= n || o >= a.ff) continue;
-      if constexpr (I8) {
-        g *= scales4(a.s_up + (size_t)e * 2 * a.ff, o, a.ff);
-        u *= scales4(a.s_up + ((size_t)e * 2 + 1) * a.ff, o, a.ff);
-      }
-      typedef T T4 __attribute__((ext_vector_type(4)));
-      T4 h;
+        for (int j = 0; j < FN; ++j) {
+          const int c = c0 + 16 * j + l16;
+          xo[j] = c < n ? (ONE ? 0u : (uint32_t)(s_slot[c] / a.topk) * (uint32_t)(a.ldx * 2)) : OOB;
+        }
+      },
+      [&](int t, const f32x4 (&acc)[2 * P][FN]) {
+        // (two places for the parts: a wave that is a tile ahead writes the other)
+        f32x4(*const sum)[2 * P * FN][64] = s_sum[ONE ? 0 : t & 1];
+        put_parts<2 * P, FN>(acc, sum, wave, lane);
+        const int c0 = t * 16 * FN;
+        for (int f = wave; f < P * FN; f += WAVES) {
+          const int c = c0 + 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
+          f32x4 g = sum_parts<WAVES, 2 * P * FN>(sum, f, lane), u = sum_parts<WAVES, 2 * P * FN>(sum, P * FN + f, lane);
+          if (c >= n || o >= a.ff) continue;
+          if constexpr (I8) {
+            g *= scales4(a.s_up + (size_t)e * 2 * a.ff, o, a.ff);
+            u *= scales4(a.s_up + ((size_t)e * 2 + 1) * a.ff, o, a.ff);
+          }
+          typedef T T4 __attribute__((ext_vector_type(4)));
+          T4 h;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) h[v] = (T)(silu_f(g[v]) * u[v]);
-      const int s = ONE ? unit : s_slot[c];
-      *reinterpret_cast<T4*>(reinterpret_cast<T*>(a.h) + (size_t)s * a.ff + o) = h;       // ff % 8 == 0
-    }
-  }
+          for (int v = 0; v < 4; ++v) h[v] = (T)(silu_f(g[v]) * u[v]);
+          const int s = ONE ? unit : s_slot[c];
+          *reinterpret_cast<T4*>(reinterpret_cast<T*>(a.h) + (size_t)s * a.ff + o) = h;       // ff % 8 == 0
+        }
+      });
 }
 
 // y[t][o] = add[t][o] + v
@@ -306,7 +334,7 @@ __device__ __forceinline__ void add_slots(const ExpertsArgs& a, int o0, bool any
 template <typename T, bool I8, int WAVES, int FM, int FN>
 __global__ __launch_bounds__(64 * WAVES) void experts_down_kernel(ExpertsArgs a, int mtile) {
   __shared__ int s_slot[EXPERTS_SLOTS];
-  __shared__ f32x4 s_sum[WAVES][FM * FN][64];
+  __shared__ f32x4 s_sum[2][WAVES][FM * FN][64];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -321,49 +349,50 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_kernel(ExpertsArgs a,
   }
   e = __builtin_amdgcn_readfirstlane(e);
   __syncthreads();
-
   constexpr int ES = I8 ? 1 : 2;
-  const char* wb[FM];
-  int wn[FM];
+  const int chunks = (n + 16 * FN - 1) / (16 * FN);
+  const char* const w0 = reinterpret_cast<const char*>(a.w_down) + (size_t)e * a.d * a.ff * ES;
+  stream_tiles<T, I8, WAVES, FM, FN>(
+      chunks, a.ff, reinterpret_cast<const char*>(a.h), wave, lane,
+      [&](int t, __amdgpu_buffer_rsrc_t (&rw)[FM], uint32_t (&vw)[FM], uint32_t (&xo)[FN]) {
+        const int c0 = t * 16 * FN;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    wb[i] = reinterpret_cast<const char*>(a.w_down) + ((size_t)e * a.d + m0 + 16 * i) * a.ff * ES;
-    wn[i] = a.d - m0 - 16 * i;
-  }
-  for (int c0 = 0; c0 < n; c0 += 16 * FN) {
-    uint32_t xo[FN];
+        for (int i = 0; i < FM; ++i) {
+          rw[i] = make_rsrc(w0 + (size_t)(m0 + 16 * i) * a.ff * ES, (uint32_t)OOB);
+          vw[i] = l16 < a.d - m0 - 16 * i ? (uint32_t)l16 * (uint32_t)(a.ff * ES) + lg * 16u : OOB;
+        }
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int c = c0 + 16 * j + l16;
-      xo[j] = c < n ? (uint32_t)s_slot[c] * (uint32_t)(a.ff * 2) : OOB;
-    }
-    f32x4 acc[FM][FN];
-    part_of_product<T, I8, WAVES, FM, FN>(wb, wn, a.ff, reinterpret_cast<const char*>(a.h), xo, wave, lane, acc);
-    if (c0 > 0) __syncthreads();
-    put_parts<FM, FN>(acc, s_sum, wave, lane);
-    for (int f = wave; f < FM * FN; f += WAVES) {
-      const int c = c0 + 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
-      f32x4 sum = sum_parts<WAVES, FM * FN>(s_sum, f, lane);
-      if (c >= n || o >= a.d) continue;
-      const int s = s_slot[c];
-      const float g = a.w[s];
-      if constexpr (I8) sum *= scales4(a.s_down + (size_t)e * a.d, o, a.d);
-      float* z = a.z + (size_t)s * a.d + o;     // d % 8 == 0
+        for (int j = 0; j < FN; ++j) {
+          const int c = c0 + 16 * j + l16;
+          xo[j] = c < n ? (uint32_t)s_slot[c] * (uint32_t)(a.ff * 2) : OOB;
+        }
+      },
+      [&](int t, const f32x4 (&acc)[FM][FN]) {
+        f32x4(*const parts_of)[FM * FN][64] = s_sum[t & 1];
+        put_parts<FM, FN>(acc, parts_of, wave, lane);
+        const int c0 = t * 16 * FN;
+        for (int f = wave; f < FM * FN; f += WAVES) {
+          const int c = c0 + 16 * (f % FN) + l16, o = m0 + 16 * (f / FN) + 4 * lg;
+          f32x4 sum = sum_parts<WAVES, FM * FN>(parts_of, f, lane);
+          if (c >= n || o >= a.d) continue;
+          const int s = s_slot[c];
+          const float g = a.w[s];
+          if constexpr (I8) sum *= scales4(a.s_down + (size_t)e * a.d, o, a.d);
+          float* z = a.z + (size_t)s * a.d + o;   // d % 8 == 0
 #pragma unroll
-      for (int v = 0; v < 4; ++v) __hip_atomic_store(z + v, sum[v] * g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-  }
+          for (int v = 0; v < 4; ++v) __hip_atomic_store(z + v, sum[v] * g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      });
   // z is written through to where every XCD sees it (stores of agent scope) and
   // has arrived there before the count goes out; the last workgroup reads it
-  // from there.  (A release fence instead writes back an XCD's whole L2, for
-  // every workgroup: 32 tokens through 60 experts took 1595 us.)
+  // from there.  (A release fence instead writes back an XCD's whole L2,
+  // for every workgroup: 32 tokens through 60 experts took 1595 us.)
   wait_vm<0>();
   bar_nofence();
   if (threadIdx.x == 0)
     s_last = __hip_atomic_fetch_add(a.done + m, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == hit - 1;
   __syncthreads();
-  if (s_last == 0) return;
-  add_slots<WAVES, 16 * FM>(a, m0, true);
+  if (s_last != 0) add_slots<WAVES, 16 * FM>(a, m0, true);
 }
 
 // The down product of a single token: 16 outputs over all of its slots, one after
@@ -429,8 +458,8 @@ static void go_up(const ExpertsArgs& a, hipStream_t s) {
 template <typename T, bool I8, int WAVES, int FM, int FN>
 static void go_down(const ExpertsArgs& a, hipStream_t s) {
   const int mtile = (a.d + 16 * FM - 1) / (16 * FM);
-  hipLaunchKernelGGL((experts_down_kernel<T, I8, WAVES, FM, FN>), dim3((unsigned)(mtile * units_of(a))),
-                     dim3(64 * WAVES), 0, s, a, mtile);
+  hipLaunchKernelGGL((experts_down_kernel<T, I8, WAVES, FM, FN>), dim3((unsigned)(mtile * units_of(a))), dim3(64 * WAVES),
+                     0, s, a, mtile);
 }
 
 // A workgroup's outputs and waves, by what was measured (us of both kernels, bf16

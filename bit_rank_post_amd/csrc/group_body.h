@@ -4,6 +4,8 @@
 #include "group_gemm.h"
 #include "tq_device.h"
 
+#include <type_traits>
+
 namespace tq {
 
 struct e4m3_t { uint8_t v; };
@@ -30,7 +32,7 @@ template <> struct Sum<i8_t> { typedef i32x4 type; };
 // agree).
 template <typename T>
 __device__ __forceinline__ typename Sum<T>::type mfma_half(u32x4 a, u32x4 b, typename Sum<T>::type c) {
-  if constexpr (sizeof(T) == 1) {
+  if constexpr (std::is_same<T, i8_t>::value) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
   } else {
     typedef typename Vec8<T>::type V8;

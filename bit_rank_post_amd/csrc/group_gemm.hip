@@ -44,8 +44,6 @@
 // that one MFMA of a SIMD takes (busy 38 % with the MFMAs' issue, and 36 %).
 #include "group_body.h"
 
-#include <type_traits>
-
 namespace tq {
 
 // The i-th group in the order of work, and its rows [lo, hi): first the groups

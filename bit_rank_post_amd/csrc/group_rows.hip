@@ -14,8 +14,6 @@
 // start and the last loads count.
 #include "group_body.h"
 
-#include <type_traits>
-
 namespace tq {
 
 // A workgroup takes 16 FM outputs x 16 FN rows; a run is D steps of 128 bytes

@@ -95,6 +95,23 @@ def test_gradient(T, k, d, zdt, ydt, want):
     assert (dz == -7).all(), "rows that no slot names, or columns beside them, were written"
 
 
+def test_more_tokens_than_workgroups():
+    """2^20 workgroups of four waves take tokens, and slots, in turns."""
+    T, d = (1 << 22) + 5, 8
+    inv = torch.arange(T - 1, -1, -1, dtype=I32, device="cuda")
+    z, dy = torch.randn((T, d), device="cuda").half(), torch.randn((T, d), device="cuda").half()
+    y, dz, dw = torch.empty_like(z), torch.zeros_like(z), torch.empty((T, 1), device="cuda")
+    tq.combine(z, inv, y)
+    assert torch.equal(y, z.flip(0))
+    tq.combine_grad(dy, inv, z=z, dz=dz, dw=dw)
+    assert torch.equal(dz, dy.flip(0))
+    p = dy.double() * z.flip(0).double()
+    assert ((dw[:, 0].double() - p.sum(1)).abs() <= (8 + 8) * U * p.abs().sum(1)).all()
+    few, k = T // 2048, 2048            # few tokens of many slots: a wave a slot
+    tq.combine_grad(dy[:few], inv[:few * k], z=z, dz=dz)
+    assert torch.equal(dz.flip(0)[:few * k], dy[:few].repeat_interleave(k, 0))
+
+
 def test_gradient_against_differences():
     """y is linear in z and in w: y(w + e) - y(w) = e dy^T dw, up to roundings."""
     T, k, d = 6, 3, 64

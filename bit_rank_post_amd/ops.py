@@ -102,6 +102,8 @@ def _ld(fn, t, name):
     rows of one element, may have any stride in torch)."""
     if t.dim() != 2:
         _refuse(fn, f"{name} must have two dimensions, not {t.dim()}")
+    if t.is_contiguous():
+        return t.shape[1]
     rows, d = t.shape
     s0, s1 = t.stride()
     if s1 != 1 and d > 1:
@@ -501,7 +503,8 @@ def _gate_up(fn, a, off):
         if groups < 1:
             _refuse(fn, "off must be [groups + 1]")
         _int32(fn, off, "off", groups + 1)
-    _fits(fn, rows, cols, groups)
+    if rows > 0x7FFFFFFF or cols > 0x7FFFFFFF or groups > 0x7FFFFFFF:
+        _fits(fn, rows, cols, groups)
     return rows, cols // 2, groups, adt, Rows(a.data_ptr(), lda)
 
 
@@ -544,25 +547,28 @@ def swiglu_grad(a, dh, da, h=None, off=None, stream=None):
 
 def _slots_of(fn, inv, T):
     """Slots of a token, from inv [T * topk] or [T][topk]."""
+    if inv.dtype is not torch.int32:
+        _refuse(fn, f"inv is {inv.dtype}, must be int32", EINVAL)
     if inv.dim() == 2:
         k = inv.shape[1]
         _shape(fn, inv, "inv", T, k)
     else:
         k = inv.numel() // T if T else 1
         _shape(fn, inv, "inv", T * k)
-    if inv.dtype is not torch.int32:
-        _refuse(fn, f"inv is {inv.dtype}, must be int32", EINVAL)
-    _dense(fn, inv, "inv")
+    if not inv.is_contiguous():
+        _dense(fn, inv, "inv")
     return k
 
 
 def _per_slot(fn, t, name, T, k):
     if t is None:
         return
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         _refuse(fn, f"{name} is {t.dtype}, must be float32", EINVAL)
-    _shape(fn, t, name, T, k)
-    _dense(fn, t, name)
+    if t.shape != (T, k):
+        _shape(fn, t, name, T, k)
+    if not t.is_contiguous():
+        _dense(fn, t, name)
 
 
 def combine(z, inv, y, w=None, add=None, stream=None):
@@ -577,10 +583,11 @@ def combine(z, inv, y, w=None, add=None, stream=None):
     rows, d = z.shape
     T = y.shape[0]
     k = _slots_of(fn, inv, T)
-    _fits(fn, T, k, d, rows)
+    if T > 0x7FFFFFFF or k > 0x7FFFFFFF or d > 0x7FFFFFFF or rows > 0x7FFFFFFF:
+        _fits(fn, T, k, d, rows)
     _per_slot(fn, w, "w", T, k)
-    desc = CombineDesc(T, k, d, rows, zdt, ydt, _ptr(inv), _ptr(w), Rows(z.data_ptr(), ldz),
-                       _mat(fn, y, "y", T, d, y.dtype), _mat(fn, add, "add", T, d, y.dtype), _ABSENT, _ABSENT, None)
+    desc = CombineDesc(T, k, d, rows, zdt, ydt, inv.data_ptr(), _ptr(w), Rows(z.data_ptr(), ldz),
+                       _mat(fn, y, "y", T, d, y.dtype), _ABSENT if add is None else _mat(fn, add, "add", T, d, y.dtype))
     _call(fn, dev, stream, ctypes.byref(desc))
 
 

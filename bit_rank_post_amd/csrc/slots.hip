@@ -116,70 +116,72 @@ __global__ __launch_bounds__(256) void slot_sum_grad_kernel(SlotSumArgs a) {
 
 // A wave takes a token of up to 512 VPT values.
 template <typename Z, typename Y, int VPT>
-__global__ __launch_bounds__(256) void slot_sum_grad_tokens_kernel(SlotSumArgs a) {
+__global__ __launch_bounds__(256) void slot_sum_grad_tokens_kernel(SlotSumArgs a, int t0) {
   const int lane = threadIdx.x & 63;
-  const long stride = (long)gridDim.x * 4;
-  for (long t = (long)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += stride) {
-    Raw8<Y> u[VPT];
-    const Y* dy = reinterpret_cast<const Y*>(a.dy) + t * a.ld_dy;
+  const long t = (long)t0 + blockIdx.x * 4u + (threadIdx.x >> 6);
+  if (t >= a.T) return;
+  Raw8<Y> u[VPT];
+  const Y* dy = reinterpret_cast<const Y*>(a.dy) + t * a.ld_dy;
+#pragma unroll
+  for (int q = 0; q < VPT; ++q)
+    if (q * 512 + lane * 8 < a.d) u[q].load(dy + q * 512 + lane * 8);
+  Raw8<Z> v[2][VPT];
+  int row[2];
+  auto request = [&](int j, int b) {
+    row[b] = j < a.topk ? slot_row(a, a.inv[t * a.topk + j]) : -1;
+    if (row[b] < 0 || a.dw == nullptr) return;
+    const Z* z = reinterpret_cast<const Z*>(a.z) + (long)row[b] * a.ldz;
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
-      if (q * 512 + lane * 8 < a.d) u[q].load(dy + q * 512 + lane * 8);
-    Raw8<Z> v[2][VPT];
-    int row[2];
-    auto request = [&](int j, int b) {
-      row[b] = j < a.topk ? slot_row(a, a.inv[t * a.topk + j]) : -1;
-      if (row[b] < 0 || a.dw == nullptr) return;
-      const Z* z = reinterpret_cast<const Z*>(a.z) + (long)row[b] * a.ldz;
+      if (q * 512 + lane * 8 < a.d) v[b][q].load(z + q * 512 + lane * 8);
+  };
+  auto slot = [&](int j, int b) {
+    const long s = t * a.topk + j;
+    float dot = 0.f;
+    if (row[b] >= 0) {
+      const float g = a.w == nullptr ? 1.f : a.w[s];
+      Z* dz = reinterpret_cast<Z*>(a.dz) + (long)row[b] * a.ld_dz;
 #pragma unroll
-      for (int q = 0; q < VPT; ++q)
-        if (q * 512 + lane * 8 < a.d) v[b][q].load(z + q * 512 + lane * 8);
-    };
-    auto slot = [&](int j, int b) {
-      const long s = t * a.topk + j;
-      float dot = 0.f;
-      if (row[b] >= 0) {
-        const float g = a.w == nullptr ? 1.f : a.w[s];
-        Z* dz = reinterpret_cast<Z*>(a.dz) + (long)row[b] * a.ld_dz;
+      for (int q = 0; q < VPT; ++q) {
+        const int c = q * 512 + lane * 8;
+        if (c >= a.d) continue;
+        if (a.dw != nullptr) {
 #pragma unroll
-        for (int q = 0; q < VPT; ++q) {
-          const int c = q * 512 + lane * 8;
-          if (c >= a.d) continue;
-          if (a.dw != nullptr) {
+          for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(u[q].get(e), v[b][q].get(e), dot);
+        }
+        if (a.dz != nullptr) {
+          float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot = __builtin_fmaf(u[q].get(e), v[b][q].get(e), dot);
-          }
-          if (a.dz != nullptr) {
-            float o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = g * u[q].get(e);
-            store8(dz + c, o);
-          }
+          for (int e = 0; e < 8; ++e) o[e] = g * u[q].get(e);
+          store8(dz + c, o);
         }
       }
-      if (a.dw != nullptr) {
-        dot = wave_sum(dot);
-        if (lane == 0) a.dw[s] = dot;
-      }
-    };
-    request(0, 0);
-    for (int j = 0; j < a.topk; j += 2) {
-      request(j + 1, 1);
-      slot(j, 0);
-      if (j + 1 >= a.topk) break;
-      request(j + 2, 0);
-      slot(j + 1, 1);
     }
+    if (a.dw != nullptr) {
+      dot = wave_sum(dot);
+      if (lane == 0) a.dw[s] = dot;
+    }
+  };
+  request(0, 0);
+  for (int j = 0; j < a.topk; j += 2) {
+    request(j + 1, 1);
+    slot(j, 0);
+    if (j + 1 >= a.topk) break;
+    request(j + 2, 0);
+    slot(j + 1, 1);
   }
 }
 
 template <typename Z, typename Y>
 static void go_sum(const SlotSumArgs& a, bool grad, hipStream_t s) {
   if (grad && a.T >= 4096 && a.d <= 4096) {
-    const long groups = ((long)a.T + 3) / 4;
-    const dim3 grid((unsigned)(groups < (1 << 20) ? groups : 1 << 20));
-    if (a.d <= 2048) hipLaunchKernelGGL((slot_sum_grad_tokens_kernel<Z, Y, 4>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((slot_sum_grad_tokens_kernel<Z, Y, 8>), grid, dim3(256), 0, s, a);
+    // (2^24 workgroups of 256 threads are a launch)
+    for (long t0 = 0; t0 < a.T; t0 += 1 << 24) {
+      const long n = a.T - t0 < (1 << 24) ? a.T - t0 : 1 << 24;
+      const dim3 grid((unsigned)((n + 3) / 4));
+      if (a.d <= 2048) hipLaunchKernelGGL((slot_sum_grad_tokens_kernel<Z, Y, 4>), grid, dim3(256), 0, s, a, (int)t0);
+      else hipLaunchKernelGGL((slot_sum_grad_tokens_kernel<Z, Y, 8>), grid, dim3(256), 0, s, a, (int)t0);
+    }
     return;
   }
   if (grad) {

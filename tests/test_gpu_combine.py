@@ -96,8 +96,9 @@ def test_gradient(T, k, d, zdt, ydt, want):
 
 
 def test_more_tokens_than_workgroups():
-    """2^20 workgroups of four waves take tokens, and slots, in turns."""
-    T, d = (1 << 22) + 5, 8
+    """A launch takes 2^24 tokens, one wave each; 2^20 workgroups of four waves take
+    slots in turns."""
+    T, d = (1 << 24) + 5, 8
     inv = torch.arange(T - 1, -1, -1, dtype=I32, device="cuda")
     z, dy = torch.randn((T, d), device="cuda").half(), torch.randn((T, d), device="cuda").half()
     y, dz, dw = torch.empty_like(z), torch.zeros_like(z), torch.empty((T, 1), device="cuda")
@@ -107,6 +108,7 @@ def test_more_tokens_than_workgroups():
     assert torch.equal(dz, dy.flip(0))
     p = dy.double() * z.flip(0).double()
     assert ((dw[:, 0].double() - p.sum(1)).abs() <= (8 + 8) * U * p.abs().sum(1)).all()
+    del p
     few, k = T // 2048, 2048            # few tokens of many slots: a wave a slot
     tq.combine_grad(dy[:few], inv[:few * k], z=z, dz=dz)
     assert torch.equal(dz.flip(0)[:few * k], dy[:few].repeat_interleave(k, 0))

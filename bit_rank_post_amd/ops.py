@@ -116,7 +116,7 @@ def _ld(fn, t, name):
 
 
 def _int32(fn, t, name, *shape):
-    if t is None:
+    if t is None or (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
         return
     if t.dtype is not torch.int32:
         _refuse(fn, f"{name} is {t.dtype}, must be int32", EINVAL)
@@ -127,9 +127,11 @@ def _int32(fn, t, name, *shape):
 def _group_desc(fn, groups, rows, d_in, d_out, act, off, src, src_div, x_rows, ldx, ldy):
     if off is None and groups != 1:
         _refuse(fn, f"off is needed with {groups} groups", EINVAL)
-    _int32(fn, off, "off", groups + 1)
-    _int32(fn, src, "src", rows)
-    if src is None and x_rows != rows:
+    if off is not None:
+        _int32(fn, off, "off", groups + 1)
+    if src is not None:
+        _int32(fn, src, "src", rows)
+    elif x_rows != rows:
         _refuse(fn, f"x has {x_rows} rows for {rows} grouped rows and no src")
     _fits(fn, groups, rows, d_in, d_out, src_div, x_rows)
     return GroupDesc(groups, rows, d_in, d_out, act, _ptr(off), _ptr(src), src_div, x_rows, ldx, ldy)
@@ -435,14 +437,14 @@ def group_slots(ids, K, off, perm, inv, ws, stream=None):
             ws.view(-1).view(torch.uint8)[:4].zero_()
 
 
-def _codes(fn, q, scale, shape):
-    """8-bit codes of the given shape and a scale for each of their rows."""
-    if q.dtype != torch.int8 or scale.dtype != torch.float32:
-        _refuse(fn, f"q is {q.dtype} and scale {scale.dtype}: int8 and float32", EINVAL)
-    _shape(fn, q, "q", *shape)
-    _shape(fn, scale, "scale", *shape[:-1])
-    _dense(fn, q, "q")
-    _dense(fn, scale, "scale")
+def _typed(fn, t, name, dtype, shape):
+    """A contiguous tensor of one type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
+        _refuse(fn, f"{name} is {t.dtype}, must be {dtype}", EINVAL)
+    _shape(fn, t, name, *shape)
+    _dense(fn, t, name)
 
 
 def int8_quant_rows(x, q, scale, stream=None):
@@ -452,16 +454,19 @@ def int8_quant_rows(x, q, scale, stream=None):
     fn = "int8_quant_rows"
     dev = _device(fn, x, q, scale)
     xdt = _float(fn, x, "x")
-    if x.dim() not in (2, 3):
-        _refuse(fn, "x must be [rows][d] or [groups][d_out][d_in]")
-    _codes(fn, q, scale, tuple(x.shape))
-    if x.dim() == 3:
+    shape = x.shape
+    if len(shape) == 2:
+        (rows, d), ldx = shape, _ld(fn, x, "x")
+    elif len(shape) == 3:
         _dense(fn, x, "x")
-        rows, d, ldx = x.shape[0] * x.shape[1], x.shape[2], x.shape[2]
+        rows, d = shape[0] * shape[1], shape[2]
+        ldx = d
     else:
-        (rows, d), ldx = x.shape, _ld(fn, x, "x")
+        _refuse(fn, "x must be [rows][d] or [groups][d_out][d_in]")
+    _typed(fn, q, "q", torch.int8, shape)
+    _typed(fn, scale, "scale", torch.float32, shape[:-1])
     _fits(fn, rows, d)
-    _call(fn, dev, stream, _ptr(x), xdt, rows, d, ldx, _ptr(q), _ptr(scale))
+    _call(fn, dev, stream, x.data_ptr(), xdt, rows, d, ldx, q.data_ptr(), scale.data_ptr())
 
 
 def int8_gemm(x, x_scale, w, w_scale, y, off=None, src=None, src_div=1, stream=None):
@@ -471,24 +476,25 @@ def int8_gemm(x, x_scale, w, w_scale, y, off=None, src=None, src_div=1, stream=N
     bfloat16 or float32.  src gathers the rows of x and of x_scale alike."""
     fn = "int8_gemm"
     dev = _device(fn, x, x_scale, w, w_scale, y, off, src)
-    if w.dim() == 2:
-        w, w_scale = w[None], w_scale[None]
-    if w.dim() != 3:
+    shape = w.shape
+    if len(shape) == 3:
+        G, d_out, d_in = shape
+    elif len(shape) == 2:
+        G, (d_out, d_in) = 1, shape
+    else:
         _refuse(fn, "w must be [groups][d_out][d_in]")
-    for name, t, dt in (("x", x, torch.int8), ("w", w, torch.int8), ("x_scale", x_scale, torch.float32),
-                        ("w_scale", w_scale, torch.float32)):
-        if t.dtype != dt:
-            _refuse(fn, f"{name} is {t.dtype}, must be {dt}", EINVAL)
-    G, d_out, d_in = w.shape
+    if x.dtype is not torch.int8:
+        _refuse(fn, f"x is {x.dtype}, must be torch.int8", EINVAL)
     ldx, ldy, ydt = _ld(fn, x, "x"), _ld(fn, y, "y"), _float(fn, y, "y")
-    _shape(fn, x, "x", x.shape[0], d_in)
-    _shape(fn, y, "y", y.shape[0], d_out)
-    _shape(fn, x_scale, "x_scale", x.shape[0])
-    _shape(fn, w_scale, "w_scale", G, d_out)
-    for name, t in (("w", w), ("x_scale", x_scale), ("w_scale", w_scale)):
-        _dense(fn, t, name)
-    d = _group_desc(fn, G, y.shape[0], d_in, d_out, TQ_F16, off, src, src_div, x.shape[0], ldx, ldy)
-    _call(fn, dev, stream, ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y), ydt)
+    x_rows, rows = x.shape[0], y.shape[0]
+    _shape(fn, x, "x", x_rows, d_in)
+    _shape(fn, y, "y", rows, d_out)
+    _typed(fn, w, "w", torch.int8, shape)
+    _typed(fn, x_scale, "x_scale", torch.float32, (x_rows,))
+    _typed(fn, w_scale, "w_scale", torch.float32, shape[:-1])
+    d = _group_desc(fn, G, rows, d_in, d_out, TQ_F16, off, src, src_div, x_rows, ldx, ldy)
+    _call(fn, dev, stream, ctypes.byref(d), x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+          y.data_ptr(), ydt)
 
 
 def _gate_up(fn, a, off):
@@ -527,7 +533,8 @@ def swiglu_int8(a, q, scale, off=None, stream=None):
     fn = "swiglu_int8"
     dev = _device(fn, a, q, scale, off)
     rows, ff, groups, adt, ra = _gate_up(fn, a, off)
-    _codes(fn, q, scale, (rows, ff))
+    _typed(fn, q, "q", torch.int8, (rows, ff))
+    _typed(fn, scale, "scale", torch.float32, (rows,))
     d = SwigluDesc(rows, ff, groups, adt, adt, _ptr(off), ra)
     _call(fn, dev, stream, ctypes.byref(d), _ptr(q), _ptr(scale))
 
@@ -560,17 +567,6 @@ def _slots_of(fn, inv, T):
     return k
 
 
-def _per_slot(fn, t, name, T, k):
-    if t is None:
-        return
-    if t.dtype is not torch.float32:
-        _refuse(fn, f"{name} is {t.dtype}, must be float32", EINVAL)
-    if t.shape != (T, k):
-        _shape(fn, t, name, T, k)
-    if not t.is_contiguous():
-        _dense(fn, t, name)
-
-
 def combine(z, inv, y, w=None, add=None, stream=None):
     """y[t] = add[t] + sum over j of w[t][j] * z[inv[t * topk + j]]: z [rows][d]
     (one row per slot, in expert order), inv int32 [T * topk] of group_slots, w
@@ -585,7 +581,8 @@ def combine(z, inv, y, w=None, add=None, stream=None):
     k = _slots_of(fn, inv, T)
     if T > 0x7FFFFFFF or k > 0x7FFFFFFF or d > 0x7FFFFFFF or rows > 0x7FFFFFFF:
         _fits(fn, T, k, d, rows)
-    _per_slot(fn, w, "w", T, k)
+    if w is not None:
+        _typed(fn, w, "w", torch.float32, (T, k))
     desc = CombineDesc(T, k, d, rows, zdt, ydt, inv.data_ptr(), _ptr(w), Rows(z.data_ptr(), ldz),
                        _mat(fn, y, "y", T, d, y.dtype), _ABSENT if add is None else _mat(fn, add, "add", T, d, y.dtype))
     _call(fn, dev, stream, ctypes.byref(desc))
@@ -607,8 +604,9 @@ def combine_grad(dy, inv, w=None, z=None, dz=None, dw=None, stream=None):
     zdt = _float(fn, rows_of, "z" if z is not None else "dz")
     rows = rows_of.shape[0]
     _fits(fn, T, k, d, rows)
-    _per_slot(fn, w, "w", T, k)
-    _per_slot(fn, dw, "dw", T, k)
+    for name, t in (("w", w), ("dw", dw)):
+        if t is not None:
+            _typed(fn, t, name, torch.float32, (T, k))
     desc = CombineDesc(T, k, d, rows, zdt, ydt, _ptr(inv), _ptr(w), _mat(fn, z, "z", rows, d, rows_of.dtype), _ABSENT,
                        _ABSENT, Rows(dy.data_ptr(), ld_dy), _mat(fn, dz, "dz", rows, d, rows_of.dtype), _ptr(dw))
     _call(fn, dev, stream, ctypes.byref(desc))
@@ -643,24 +641,18 @@ def experts_forward(x, ids, w, w_up, w_down, y, ws, s_up=None, s_down=None, add=
     k, (E, _, ff) = ids.shape[1], w_down.shape
     _fits(fn, T, k, E, d, ff)
     _int32(fn, ids, "ids", T, k)
-    _per_slot(fn, w, "w", T, k)
+    _typed(fn, w, "w", torch.float32, (T, k))
     _shape(fn, y, "y", T, d)
-    _shape(fn, w_up, "w_up", E, 2 * ff, d)
-    _shape(fn, w_down, "w_down", E, d, ff)
-    if (s_up is None) != (s_down is None):
-        _refuse(fn, "s_up and s_down go together", EINVAL)
-    want = x.dtype if s_up is None else torch.int8
-    for name, t in (("w_up", w_up), ("w_down", w_down)):
-        if t.dtype != want:
-            _refuse(fn, f"{name} is {t.dtype}, must be {want}", EINVAL)
-        _dense(fn, t, name)
-    for name, t, n in (("s_up", s_up, 2 * ff), ("s_down", s_down, d)):
-        if t is None:
-            continue
-        if t.dtype != torch.float32:
-            _refuse(fn, f"{name} is {t.dtype}, must be float32", EINVAL)
-        _shape(fn, t, name, E, n)
-        _dense(fn, t, name)
+    want = x.dtype
+    if s_up is not None or s_down is not None:
+        if s_up is None or s_down is None:
+            _refuse(fn, "s_up and s_down go together", EINVAL)
+        want = torch.int8
+    _typed(fn, w_up, "w_up", want, (E, 2 * ff, d))
+    _typed(fn, w_down, "w_down", want, (E, d, ff))
+    if s_up is not None:
+        _typed(fn, s_up, "s_up", torch.float32, (E, 2 * ff))
+        _typed(fn, s_down, "s_down", torch.float32, (E, d))
     _dense(fn, ws, "ws")
     desc = ExpertsDesc(T, k, E, d, ff, _DT[x.dtype], ydt, _ptr(ids), _ptr(w), _ptr(w_up), _ptr(w_down), _ptr(s_up),
                        _ptr(s_down), Rows(x.data_ptr(), ldx), Rows(y.data_ptr(), ldy),

@@ -263,8 +263,8 @@ def layer_args(T=4, k=2, E=8, d=64, ff=32, **kw):
     (lambda: tq.int8_quant_rows(meta(BIG, 16), meta(BIG, 16, dtype=I8), meta(BIG, dtype=F32)), "32 bits"),
     (lambda: tq.int8_quant_rows(meta(1 << 20, 1 << 13, 16), meta(1 << 20, 1 << 13, 16, dtype=I8),
                                 meta(1 << 20, 1 << 13, dtype=F32)), "32 bits"),
-    (lambda: tq.int8_quant_rows(meta(4, 16), meta(4, 16), meta(4, dtype=F32)), "int8 and float32"),
-    (lambda: tq.int8_quant_rows(meta(4, 16), meta(4, 16, dtype=I8), meta(4)), "int8 and float32"),
+    (lambda: tq.int8_quant_rows(meta(4, 16), meta(4, 16), meta(4, dtype=F32)), "q is .*must be torch.int8"),
+    (lambda: tq.int8_quant_rows(meta(4, 16), meta(4, 16, dtype=I8), meta(4)), "scale is .*must be torch.float32"),
     (lambda: tq.int8_quant_rows(meta(4, 16), meta(4, 32, dtype=I8), meta(4, dtype=F32)), "must be"),
     (lambda: tq.int8_quant_rows(meta(4, 16), meta(4, 16, dtype=I8), meta(5, dtype=F32)), "must be"),
     (lambda: tq.int8_quant_rows(meta(4, 16, dtype="float64"), meta(4, 16, dtype=I8), meta(4, dtype=F32)), "float16, bfloat16"),

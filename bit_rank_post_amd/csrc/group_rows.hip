@@ -11,7 +11,7 @@
 // wave order.  60 experts of 2048 -> 1408, 32 tokens top-4, f16: 57 us, 5.4 TB/s
 // of the weights of the 53 experts that have rows (a plain read of a larger
 // buffer: 5.5); one row through 4096 -> 14336 in e4m3: 15 us, 4 TB/s, where the
-// start and the last loads count.
+// start and the last loads count; in 8-bit integers 13.5 us.
 #include "group_body.h"
 
 namespace tq {

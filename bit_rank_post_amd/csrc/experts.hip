@@ -386,7 +386,10 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_kernel(ExpertsArgs a,
   // z is written through to where every XCD sees it (stores of agent scope) and
   // has arrived there before the count goes out; the last workgroup reads it
   // from there.  (A release fence instead writes back an XCD's whole L2,
-  // for every workgroup: 32 tokens through 60 experts took 1595 us.)
+  // for every workgroup: 32 tokens through 60 experts took 1595 us.)  The wait
+  // is no memory operation to the compiler: the empty asm keeps the stores ahead
+  // of it, as the one in the barrier keeps the count behind it.
+  asm volatile("" ::: "memory");
   wait_vm<0>();
   bar_nofence();
   if (threadIdx.x == 0)

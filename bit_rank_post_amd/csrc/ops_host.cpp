@@ -512,6 +512,10 @@ tq_status check_same_rows(const tq_rows& out, long ldo, tq_dtype to, const char*
     return fail(TQ_EINVAL, "%s in place of %s with another type or row stride", out_name, in_name);
   return TQ_OK;
 }
+// the up matrix's half of rows of a or da
+tq_rows up_half(const tq_rows& a, int ff, tq_dtype t) {
+  return {a.p ? reinterpret_cast<char*>(a.p) + (size_t)ff * size_of(t) : nullptr, a.ld};
+}
 tq_status check_swiglu(const tq_swiglu_desc* d, SwigluArgs* a) {
   if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
   if (d->rows < 0) return fail(TQ_ESHAPE, "rows = %d", d->rows);
@@ -537,6 +541,7 @@ tq_status tq_swiglu(const tq_swiglu_desc* d, void* stream) {
   TRY(check_swiglu(d, &a));
   TRY(check_rows(d->h, "h", d->rows > 0, d->ff, d->h_dtype, &a.ldh));
   TRY(check_same_rows(d->h, a.ldh, d->h_dtype, "h", d->a, a.lda, d->a_dtype, "a"));
+  TRY(check_same_rows(d->h, a.ldh, d->h_dtype, "h", up_half(d->a, d->ff, d->a_dtype), a.lda, d->a_dtype, "a's second half"));
   if (d->rows == 0) return TQ_OK;
   a.h = d->h.p;
   launch_swiglu(a, (int)d->a_dtype, (int)d->h_dtype, reinterpret_cast<hipStream_t>(stream));
@@ -571,9 +576,10 @@ tq_status tq_swiglu_grad(const tq_swiglu_desc* d, void* stream) {
   TRY(check_rows(d->h, "h", false, d->ff, d->a_dtype, &a.ldh));
   TRY(check_same_rows(d->da, a.ldda, d->a_dtype, "da", d->a, a.lda, d->a_dtype, "a"));
   TRY(check_same_rows(d->h, a.ldh, d->a_dtype, "h", d->dh, a.lddh, d->h_dtype, "dh"));
+  TRY(check_same_rows(d->h, a.ldh, d->a_dtype, "h", up_half(d->a, d->ff, d->a_dtype), a.lda, d->a_dtype, "a's second half"));
   if (d->rows == 0) return TQ_OK;
   TRY(check_apart(d->da.p, d->dh.p, d->h.p));
-  TRY(check_apart(d->h.p, d->a.p, nullptr));
+  TRY(check_apart(d->h.p, d->a.p, up_half(d->da, d->ff, d->a_dtype).p));
   a.h = d->h.p;
   a.dh = d->dh.p;
   a.da = d->da.p;

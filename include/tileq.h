@@ -401,8 +401,8 @@ tq_status tq_int8_quant_rows(const void *x, tq_dtype x_dtype, int32_t rows, int3
  *          not read)
  *   q      DEVICE int8 [rows][ff], scale DEVICE f32 [rows]
  * ld 0 = dense; ff % 8 == 0 (tq_swiglu_int8: % 16, ff < 131072); rows 16-byte
- * aligned.  h may be a's first or second half, da may be a, and the gradient's
- * h may be dh (one type, the same rows with the same stride).
+ * aligned.  tq_swiglu's h may be a's first or second half, da may be a, and the
+ * gradient's h may be dh (one type, the same rows with the same stride).
  * Errors: TQ_EINVAL (NULL or misaligned pointers, dtypes), TQ_ESHAPE, TQ_EHIP. */
 typedef struct {
   int32_t rows, ff, groups;

@@ -504,11 +504,11 @@ tq_status tq_int8_quant_rows(const void* x, tq_dtype x_dtype, int32_t rows, int3
 }  // extern "C"
 
 namespace {
-// an output in the place of an input: the same type and stride, or rows are
-// written where others, not yet read, lie
-tq_status check_same_rows(const tq_rows& out, long ldo, tq_dtype to, const char* out_name, const tq_rows& in, long ldi,
-                          tq_dtype ti, const char* in_name) {
-  if (out.p && out.p == in.p && (ldo != ldi || to != ti))
+// an output in the place of an input: the same type and, of more rows than one,
+// the same stride, or rows are written where others, not yet read, lie
+tq_status check_same_rows(int rows, const tq_rows& out, long ldo, tq_dtype to, const char* out_name, const tq_rows& in,
+                          long ldi, tq_dtype ti, const char* in_name) {
+  if (out.p && out.p == in.p && (to != ti || (rows > 1 && ldo != ldi)))
     return fail(TQ_EINVAL, "%s in place of %s with another type or row stride", out_name, in_name);
   return TQ_OK;
 }
@@ -540,8 +540,8 @@ tq_status tq_swiglu(const tq_swiglu_desc* d, void* stream) {
   SwigluArgs a{};
   TRY(check_swiglu(d, &a));
   TRY(check_rows(d->h, "h", d->rows > 0, d->ff, d->h_dtype, &a.ldh));
-  TRY(check_same_rows(d->h, a.ldh, d->h_dtype, "h", d->a, a.lda, d->a_dtype, "a"));
-  TRY(check_same_rows(d->h, a.ldh, d->h_dtype, "h", up_half(d->a, d->ff, d->a_dtype), a.lda, d->a_dtype, "a's second half"));
+  TRY(check_same_rows(d->rows, d->h, a.ldh, d->h_dtype, "h", d->a, a.lda, d->a_dtype, "a"));
+  TRY(check_same_rows(d->rows, d->h, a.ldh, d->h_dtype, "h", up_half(d->a, d->ff, d->a_dtype), a.lda, d->a_dtype, "a's second half"));
   if (d->rows == 0) return TQ_OK;
   a.h = d->h.p;
   launch_swiglu(a, (int)d->a_dtype, (int)d->h_dtype, reinterpret_cast<hipStream_t>(stream));
@@ -574,9 +574,9 @@ tq_status tq_swiglu_grad(const tq_swiglu_desc* d, void* stream) {
   TRY(check_rows(d->dh, "dh", d->rows > 0, d->ff, d->h_dtype, &a.lddh));
   TRY(check_rows(d->da, "da", d->rows > 0, 2 * d->ff, d->a_dtype, &a.ldda));
   TRY(check_rows(d->h, "h", false, d->ff, d->a_dtype, &a.ldh));
-  TRY(check_same_rows(d->da, a.ldda, d->a_dtype, "da", d->a, a.lda, d->a_dtype, "a"));
-  TRY(check_same_rows(d->h, a.ldh, d->a_dtype, "h", d->dh, a.lddh, d->h_dtype, "dh"));
-  TRY(check_same_rows(d->h, a.ldh, d->a_dtype, "h", up_half(d->a, d->ff, d->a_dtype), a.lda, d->a_dtype, "a's second half"));
+  TRY(check_same_rows(d->rows, d->da, a.ldda, d->a_dtype, "da", d->a, a.lda, d->a_dtype, "a"));
+  TRY(check_same_rows(d->rows, d->h, a.ldh, d->a_dtype, "h", d->dh, a.lddh, d->h_dtype, "dh"));
+  TRY(check_same_rows(d->rows, d->h, a.ldh, d->a_dtype, "h", up_half(d->a, d->ff, d->a_dtype), a.lda, d->a_dtype, "a's second half"));
   if (d->rows == 0) return TQ_OK;
   TRY(check_apart(d->da.p, d->dh.p, d->h.p));
   TRY(check_apart(d->h.p, d->a.p, up_half(d->da, d->ff, d->a_dtype).p));
@@ -621,7 +621,7 @@ tq_status tq_combine(const tq_combine_desc* d, void* stream) {
   TRY(check_rows(d->z, "z", d->T > 0 && d->rows > 0, d->d, d->z_dtype, &a.ldz));
   TRY(check_rows(d->y, "y", d->T > 0, d->d, d->y_dtype, &a.ldy));
   TRY(check_rows(d->add, "add", false, d->d, d->y_dtype, &a.ld_add));
-  TRY(check_same_rows(d->y, a.ldy, d->y_dtype, "y", d->add, a.ld_add, d->y_dtype, "add"));
+  TRY(check_same_rows(d->T, d->y, a.ldy, d->y_dtype, "y", d->add, a.ld_add, d->y_dtype, "add"));
   if (d->T == 0) return TQ_OK;
   TRY(check_apart(d->y.p, d->z.p, d->w));
   a.z = d->z.p;
@@ -639,7 +639,7 @@ tq_status tq_combine_grad(const tq_combine_desc* d, void* stream) {
   TRY(check_rows(d->dy, "dy", d->T > 0, d->d, d->y_dtype, &a.ld_dy));
   TRY(check_rows(d->z, "z", some && d->dw != nullptr, d->d, d->z_dtype, &a.ldz));
   TRY(check_rows(d->dz, "dz", false, d->d, d->z_dtype, &a.ld_dz));
-  TRY(check_same_rows(d->dz, a.ld_dz, d->z_dtype, "dz", d->z, a.ldz, d->z_dtype, "z"));
+  TRY(check_same_rows(d->rows, d->dz, a.ld_dz, d->z_dtype, "dz", d->z, a.ldz, d->z_dtype, "z"));
   if (d->T == 0) return TQ_OK;
   TRY(check_apart(d->dz.p, d->dy.p, d->w));
   TRY(check_apart(d->dw, d->w, d->dy.p));
@@ -711,7 +711,7 @@ tq_status tq_experts_forward(const tq_experts_desc* d, void* ws, size_t ws_bytes
   if (!aligned(d->y.p, es) || !aligned(d->add.p, es)) return fail(TQ_EINVAL, "y or add not aligned to its type");
   if (!aligned(d->ids, 4) || !aligned(d->w, 4) || !aligned(d->s_up, 4) || !aligned(d->s_down, 4))
     return fail(TQ_EINVAL, "ids, w and scales must be 4-byte aligned");
-  TRY(check_same_rows(d->y, a.ldy, d->y_dtype, "y", d->add, a.ld_add, d->y_dtype, "add"));
+  TRY(check_same_rows(d->T, d->y, a.ldy, d->y_dtype, "y", d->add, a.ld_add, d->y_dtype, "add"));
   TRY(check_apart(d->y.p, d->w_up, d->w_down));
   TRY(check_apart(d->y.p, d->ids, d->w));
   const ExpertsPlan p = plan_experts(d->T, d->topk, d->d, d->ff);

@@ -552,15 +552,19 @@ def swiglu_grad(a, dh, da, h=None, off=None, stream=None):
     _call(fn, dev, stream, ctypes.byref(d))
 
 
-def _slots_of(fn, inv, T):
-    """Slots of a token, from inv [T * topk] or [T][topk]."""
+def _slots_of(fn, inv, T, *weights):
+    """Slots of a token, from inv [T * topk] or [T][topk]; without tokens from
+    weights [0][topk], where there are any."""
     if inv.dtype is not torch.int32:
         _refuse(fn, f"inv is {inv.dtype}, must be int32", EINVAL)
     if inv.dim() == 2:
         k = inv.shape[1]
         _shape(fn, inv, "inv", T, k)
     else:
-        k = inv.numel() // T if T else 1
+        if T:
+            k = inv.numel() // T
+        else:
+            k = next((w.shape[1] for w in weights if w is not None and w.dim() == 2), 1)
         _shape(fn, inv, "inv", T * k)
     if not inv.is_contiguous():
         _dense(fn, inv, "inv")
@@ -578,7 +582,7 @@ def combine(z, inv, y, w=None, add=None, stream=None):
     zdt, ldz, ydt = _float(fn, z, "z"), _ld(fn, z, "z"), _float(fn, y, "y")
     rows, d = z.shape
     T = y.shape[0]
-    k = _slots_of(fn, inv, T)
+    k = _slots_of(fn, inv, T, w)
     if T > 0x7FFFFFFF or k > 0x7FFFFFFF or d > 0x7FFFFFFF or rows > 0x7FFFFFFF:
         _fits(fn, T, k, d, rows)
     if w is not None:
@@ -597,7 +601,7 @@ def combine_grad(dy, inv, w=None, z=None, dz=None, dw=None, stream=None):
     dev = _device(fn, dy, inv, w, z, dz, dw)
     ydt, ld_dy = _float(fn, dy, "dy"), _ld(fn, dy, "dy")
     T, d = dy.shape
-    k = _slots_of(fn, inv, T)
+    k = _slots_of(fn, inv, T, w, dw)
     rows_of = z if z is not None else dz
     if rows_of is None or (dw is not None and z is None):
         _refuse(fn, "dz or dw is needed, and z for dw", EINVAL)

@@ -635,12 +635,13 @@ tq_status tq_combine_grad(const tq_combine_desc* d, void* stream) {
   SlotSumArgs a{};
   TRY(check_combine(d, &a));
   const bool some = d->T > 0 && d->rows > 0;
-  if (d->T > 0 && !d->dz.p && !d->dw) return fail(TQ_EINVAL, "neither dz nor dw is asked for");
+  // (a dz without rows may well be NULL)
+  if (some && !d->dz.p && !d->dw) return fail(TQ_EINVAL, "neither dz nor dw is asked for");
   TRY(check_rows(d->dy, "dy", d->T > 0, d->d, d->y_dtype, &a.ld_dy));
   TRY(check_rows(d->z, "z", some && d->dw != nullptr, d->d, d->z_dtype, &a.ldz));
   TRY(check_rows(d->dz, "dz", false, d->d, d->z_dtype, &a.ld_dz));
   TRY(check_same_rows(d->rows, d->dz, a.ld_dz, d->z_dtype, "dz", d->z, a.ldz, d->z_dtype, "z"));
-  if (d->T == 0) return TQ_OK;
+  if (d->T == 0 || (!some && !d->dw)) return TQ_OK;
   TRY(check_apart(d->dz.p, d->dy.p, d->w));
   TRY(check_apart(d->dw, d->w, d->dy.p));
   a.z = d->z.p;

@@ -702,7 +702,9 @@ tq_status tq_experts_forward(const tq_experts_desc* d, void* ws, size_t ws_bytes
   ExpertsArgs a{};
   TRY(check_rows(d->x, "x", d->T > 0, d->d, d->act, &a.ldx));
   if (d->T == 0) return TQ_OK;
-  if (a.ldx * 2 * d->T >= 0x7FFFFFF0L) return fail(TQ_EUNSUPPORTED, "x of %ld bytes >= 2^31", a.ldx * 2 * d->T);
+  // (a product with the stride could pass 64 bits)
+  if (a.ldx > 0x7FFFFFEFL / 2 / d->T)
+    return fail(TQ_EUNSUPPORTED, "x of %d rows of stride %ld: 2^31 bytes or more", d->T, a.ldx);
   a.ldy = d->y.ld ? d->y.ld : d->d;
   a.ld_add = d->add.ld ? d->add.ld : d->d;
   if (a.ldy < d->d || a.ld_add < d->d) return fail(TQ_ESHAPE, "row stride of y or add below d = %d", d->d);

@@ -93,8 +93,10 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(SwigluArgs a, int r0, 
     const float s = sigmoid(g[j], &rest), gs = g[j] * s;
     h[j] = gs * u[j];
     const float du = dh[j] * gs;
-    // s (1 + g (1 - s)) = s + g s (1 - s)
-    g[j] = dh[j] * u[j] * __builtin_fmaf(gs, rest, s);
+    // s (1 + g (1 - s)) = s + g s (1 - s); the larger factor meets it first, or a
+    // product on the way could leave f32 where the gradient does not
+    const bool up = __builtin_fabsf(u[j]) > __builtin_fabsf(dh[j]);
+    g[j] = __builtin_fmaf(gs, rest, s) * (up ? u[j] : dh[j]) * (up ? dh[j] : u[j]);
     u[j] = du;
   }
   A* o = reinterpret_cast<A*>(a.da) + row * a.ldda + c;

@@ -596,7 +596,10 @@ def combine_grad(dy, inv, w=None, z=None, dz=None, dw=None, stream=None):
     """Gradients of combine: dz[inv[t * topk + j]] = w[t][j] * dy[t] (rows that
     no slot names are left as they are) and dw[t][j] = dy[t] . z[inv[t * topk +
     j]] (0 for a slot with inv outside [0, rows)), each None when not wanted;
-    dw needs z.  dz may be z.  The gradient of add is dy."""
+    dw needs z.  dz may be z.  The gradient of add is dy.  For rows that one slot
+    names, as those of group_slots: dz adds nothing up, each value of a row that
+    more slots name is that of any one of them (and dw of those slots is not
+    defined where dz is z)."""
     fn = "combine_grad"
     dev = _device(fn, dy, inv, w, z, dz, dw)
     ydt, ld_dy = _float(fn, dy, "dy"), _ld(fn, dy, "dy")

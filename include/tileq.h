@@ -420,8 +420,11 @@ tq_status tq_swiglu_grad(const tq_swiglu_desc *d, void *stream);
  * and its gradient, each output NULL when not wanted:
  *   dz[inv[t topk + j]] = w[t][j] dy[t],  dw[t][j] = dy[t] . z[inv[t topk + j]]
  * A slot whose inv lies outside 0 .. rows-1 adds nothing (whatever its w), and
- * its dw is 0; rows of dz that no slot names are left as they are.  (Two slots
- * of one row: dz holds one of the two.)  Sums in f32, in the order of j.
+ * its dw is 0; rows of dz that no slot names are left as they are.  Sums in f32,
+ * in the order of j.  The gradient is for rows that one slot names, as those of
+ * tq_group_slots: nothing is added up in dz, so each value of a row that more
+ * slots name is that of any one of them, and with dz in the place of z the dw
+ * of those slots is not defined.
  * Without w, y of rows of gradients is the gradient of gathering rows from x.
  *   z, dz DEVICE z_dtype [rows][ld]; y, add, dy DEVICE y_dtype [T][ld], d values
  *   inv DEVICE int32 [T][topk]; w, dw DEVICE f32 [T][topk]

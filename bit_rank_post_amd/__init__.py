@@ -32,7 +32,7 @@ EXPORTS = ["tq_layer_create", "tq_upload_proj", "tq_upload_shared_expert",
            "tq_norm_residual_grad", "tq_group_slots_workspace_size", "tq_group_slots",
            "tq_block_workspace_size", "tq_block_forward", "tq_int8_gemm", "tq_debug_int8_kernel",
            "tq_int8_quant_rows", "tq_swiglu", "tq_swiglu_int8", "tq_swiglu_grad", "tq_combine", "tq_combine_grad",
-           "tq_experts_workspace_size", "tq_experts_forward"]
+           "tq_experts_workspace_size", "tq_experts_forward", "tq_debug_experts_kernels"]
 STAGES = ["route", "row_exponent", "column_stage_in", "gemm_in", "column_stage_down",
           "shared_expert", "gemm_down", "combine"]
 
@@ -169,6 +169,7 @@ def lib():
         L.tq_combine.argtypes = [pc, vp]
         L.tq_combine_grad.argtypes = [pc, vp]
         L.tq_experts_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.tq_debug_experts_kernels.argtypes = [i32] * 6 + [pi, pi, pi]
         L.tq_experts_forward.argtypes = [ctypes.POINTER(ExpertsDesc), vp, sz, vp]
         L.tq_norm_residual.argtypes = [ctypes.POINTER(NormDesc), vp]
         L.tq_norm_grad_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]

@@ -486,34 +486,41 @@ static void go_down(const ExpertsArgs& a, hipStream_t s) {
 // else 64 (128 tokens: 957; with 32 1007).  An expert with more slots goes over its
 // weights again.  The workgroups there: 32 outputs and 4 waves up, 64 and 8 (with 64
 // columns 4) down.
+ExpertsPick choose_experts(const ExpertsArgs& a, bool int8) {
+  const int units = units_of(a), S = a.T * a.topk, ES = int8 ? 1 : 2;
+  const int up_steps = (a.d * ES + 127) / 128, down_steps = (a.ff * ES + 127) / 128;
+  if (a.T == 1) return {1, {16, up_steps >= 32 ? 8 : 4}, {16, experts_tiles(a.d) >= 256 ? 8 : 16}};
+  if (a.T > 32 && S > 24 * a.experts) return {64, {32, 4}, {64, 4}};
+  if (a.T > 16 && S > 10 * a.experts) return {32, {32, 4}, {64, 8}};
+  ExpertsPick p{16, {32, 4}, {int8 ? 32 : 16, 4}};
+  if (up_steps >= 64) p.up = {16, 8};
+  else if (up_steps < 32) p.up = {16, 4};
+  else if (units * ((a.ff + 31) / 32) < 512) p.up = {32, 8};
+  if (down_steps >= 64 || units * ((a.d + 31) / 32) < 512) p.down = {32, 8};
+  return p;
+}
+
 template <typename T, bool I8>
 static void go_layer(const ExpertsArgs& a, hipStream_t s) {
-  const int units = units_of(a), S = a.T * a.topk, ES = I8 ? 1 : 2;
-  const int up_steps = (a.d * ES + 127) / 128, down_steps = (a.ff * ES + 127) / 128;
-  if (a.T == 1) {
-    if (up_steps >= 32) go_up<T, I8, 8, 1, 1, true>(a, s);
+  const ExpertsPick p = choose_experts(a, I8);
+  if (p.columns == 1) {
+    if (p.up.waves == 8) go_up<T, I8, 8, 1, 1, true>(a, s);
     else go_up<T, I8, 4, 1, 1, true>(a, s);
-    const int n = experts_tiles(a.d);
-    if (n >= 256) hipLaunchKernelGGL((experts_down_one_kernel<T, I8, 8>), dim3((unsigned)n), dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((experts_down_one_kernel<T, I8, 16>), dim3((unsigned)n), dim3(1024), 0, s, a);
-    return;
-  }
-  if (a.T > 32 && S > 24 * a.experts) {
+    const dim3 grid((unsigned)experts_tiles(a.d));
+    if (p.down.waves == 8) hipLaunchKernelGGL((experts_down_one_kernel<T, I8, 8>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((experts_down_one_kernel<T, I8, 16>), grid, dim3(1024), 0, s, a);
+  } else if (p.columns == 64) {
     go_up<T, I8, 4, 2, 4>(a, s);
     go_down<T, I8, 4, 4, 4>(a, s);
-    return;
-  }
-  if (a.T > 16 && S > 10 * a.experts) {
+  } else if (p.columns == 32) {
     go_up<T, I8, 4, 2, 2>(a, s);
     go_down<T, I8, 8, 4, 2>(a, s);
-    return;
+  } else {
+    if (p.up.outputs == 16) p.up.waves == 8 ? go_up<T, I8, 8, 1, 1>(a, s) : go_up<T, I8, 4, 1, 1>(a, s);
+    else p.up.waves == 8 ? go_up<T, I8, 8, 2, 1>(a, s) : go_up<T, I8, 4, 2, 1>(a, s);
+    if (p.down.waves == 8) go_down<T, I8, 8, 2, 1>(a, s);
+    else go_down<T, I8, 4, I8 ? 2 : 1, 1>(a, s);
   }
-  if (up_steps >= 64) go_up<T, I8, 8, 1, 1>(a, s);
-  else if (up_steps < 32) go_up<T, I8, 4, 1, 1>(a, s);
-  else if (units * ((a.ff + 31) / 32) < 512) go_up<T, I8, 8, 2, 1>(a, s);
-  else go_up<T, I8, 4, 2, 1>(a, s);
-  if (down_steps >= 64 || units * ((a.d + 31) / 32) < 512) go_down<T, I8, 8, 2, 1>(a, s);
-  else go_down<T, I8, 4, I8 ? 2 : 1, 1>(a, s);
 }
 
 void launch_experts(const ExpertsArgs& a, int act, bool int8, hipStream_t s) {

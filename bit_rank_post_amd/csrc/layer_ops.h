@@ -72,6 +72,14 @@ struct ExpertsArgs {
 };
 constexpr int EXPERTS_SLOTS = 1024;      // slots that a call may have
 __host__ __device__ inline int experts_tiles(int d) { return (d + 15) / 16; }
+// The kernels of a call (by sizes alone): columns that a workgroup takes at a time
+// (1: those of a single token), outputs and waves of a workgroup of either.
+struct ExpertsKernel { int outputs, waves; };
+struct ExpertsPick {
+  int columns;
+  ExpertsKernel up, down;
+};
+ExpertsPick choose_experts(const ExpertsArgs& a, bool int8);
 // act: 0 f16, 1 bf16; int8: weights in 8-bit integers
 void launch_experts(const ExpertsArgs& a, int act, bool int8, hipStream_t s);
 

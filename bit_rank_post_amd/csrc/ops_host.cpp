@@ -692,6 +692,26 @@ tq_status tq_experts_workspace_size(int32_t T, int32_t topk, int32_t experts, in
   return TQ_OK;
 }
 
+tq_status tq_debug_experts_kernels(int32_t T, int32_t topk, int32_t experts, int32_t d, int32_t ff, int32_t int8,
+                                   int32_t* columns, int32_t up[2], int32_t down[2]) {
+  if (!columns || !up || !down) return fail(TQ_EINVAL, "columns, up or down is NULL");
+  TRY(check_experts_sizes(T, topk, experts, d, ff, int8 ? 16 : 8));
+  if (T < 1) return fail(TQ_ESHAPE, "T = %d", T);
+  ExpertsArgs a{};
+  a.T = T;
+  a.topk = topk;
+  a.experts = experts;
+  a.d = d;
+  a.ff = ff;
+  const ExpertsPick p = choose_experts(a, int8 != 0);
+  *columns = p.columns;
+  up[0] = p.up.outputs;
+  up[1] = p.up.waves;
+  down[0] = p.down.outputs;
+  down[1] = p.down.waves;
+  return TQ_OK;
+}
+
 tq_status tq_experts_forward(const tq_experts_desc* d, void* ws, size_t ws_bytes, void* stream) {
   if (!d) return fail(TQ_EINVAL, "descriptor is NULL");
   if (d->act != TQ_F16 && d->act != TQ_BF16) return fail(TQ_EINVAL, "act must be TQ_F16 or TQ_BF16");

@@ -480,6 +480,12 @@ tq_status tq_experts_workspace_size(int32_t T, int32_t topk, int32_t experts, in
                                     size_t *bytes);
 tq_status tq_experts_forward(const tq_experts_desc *d, void *ws, size_t ws_bytes, void *stream);
 
+/* Test hook: the kernels that a call of these sizes takes (T >= 1; int8: 8-bit
+ * weights): columns at a time (1: a single token's kernels), and outputs and
+ * waves of a workgroup of the up and of the down kernel. */
+tq_status tq_debug_experts_kernels(int32_t T, int32_t topk, int32_t experts, int32_t d, int32_t ff, int32_t int8,
+                                   int32_t *columns, int32_t up[2], int32_t down[2]);
+
 /* Norms before and after a block, with its gate and residual scale:
  *   p(b) = w_post * b * r1,  r1 = (mean(b^2) + eps)^-1/2     (p(b) = b without w_post)
  *   y    = x + alpha * gate * p(b)                            (y = x without b)

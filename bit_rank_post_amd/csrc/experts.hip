@@ -21,9 +21,9 @@
 // counters to zero.  A single token's down workgroups go over all its slots
 // instead.
 //
-// 32 tokens through four of 60 experts of 2048 -> 1408, f16: 171 us, 5.4 TB/s of the
-// 53 experts' weights (a plain read of a larger buffer: 5.5); one token through two
-// of eight of 4096 -> 14336 in 8 bits: 71 us, 5.0 TB/s.
+// A call for 32 tokens through four of 60 experts of 2048 -> 1408, f16: 176 us, 5.2
+// TB/s of the 53 experts' weights (a plain read of a larger buffer: 5.5); for one token
+// through two of eight of 4096 -> 14336 in 8 bits: 74 us, 4.7 TB/s.
 //
 // 8-bit weights (integers with an f32 scale for each output) are unpacked to
 // the activations' type, exactly, next to the MFMA; the scale meets the sum.
@@ -465,27 +465,37 @@ static void go_down(const ExpertsArgs& a, hipStream_t s) {
                      0, s, a, mtile);
 }
 
-// A workgroup's outputs and waves, by what was measured (us of both kernels, bf16
-// weights; k in steps of 128 bytes):
+// A workgroup's outputs and waves, by what was measured (us of a call, bf16, k in
+// steps of 128 bytes; the kernel that is taken first, then the others on the same
+// inputs; "large": experts of 4096 -> 14336, "small": of 2048 -> 1408):
 //   one   a single token: no slots to look for, and the down kernel takes 16 outputs
-//         of all its slots (8-bit, 4 of 60 experts of 2048 -> 1408: 16, by the kernels
-//         below 17; 8 of 16 of 5120 -> 1536: 49, 61; one of 32 of 4096 -> 4096 in 16 bits:
-//         25, 30).  Up 8 waves from 32 steps (8 of 64 of 2048 -> 1024: 28; 4 waves 29),
-//         else 4 (8-bit, 60 experts: 15.7; 8 waves 15.9); down 8 waves from 256 workgroups
-//         (5120: 50; 16 waves 53), else 16 (2048: 15.7; 8 waves 16.3)
-//   up    from 64 steps 16 outputs, 8 waves (8 experts of 4096 -> 14336, 8 tokens:
-//         428; 4 waves 445, 32 outputs 459); from 32 steps 32 outputs, 4 waves (8-bit,
-//         the same: 248; 16 outputs 254), 8 below 512 workgroups; below 16 outputs, 4
-//         waves (8-bit 60 experts of 2048 -> 1408, 32 tokens: 115; 32 outputs 124)
-//   down  from 64 steps or below 512 workgroups 32 outputs, 8 waves (32 tokens
-//         through 8 experts of 14336 -> 4096: 487; 4 waves 490, 64 outputs 489); else 4
-//         waves and 16 outputs (64 experts of 1408 -> 2048, 64 tokens: 233; 32
-//         outputs 240) or, in 8 bits, 32 (32 tokens: 109; 16 outputs 116)
-// Columns: 16 up to 10 slots an expert on average (32 tokens through 2 of 8 experts:
-// 500, with 32 columns 516), 32 up to 24 (64 tokens: 654; with 16 702, with 64 712),
-// else 64 (128 tokens: 957; with 32 1007).  An expert with more slots goes over its
+//         of all its slots (8-bit, 4 of 60 small experts: 15.7, by the kernels below
+//         17.7; 8 of 16 of 5120 -> 1536: 49.6, 57.1; one of 32 of 4096 -> 4096 in 16 bits:
+//         24.7, 29.8).  Up 8 waves from 32 steps (2 of 8 large ones in 16 bits: 121, 4
+//         waves 125; 4 of 60 small ones 21.0, 20.3), else 4 (8-bit, the 60 small: 15.7,
+//         8 waves 16.1); down 8 waves from 256 workgroups (5120: 49.5, 16 waves 51.8;
+//         large ones 71.3, 70.9), else 16 (8-bit small: 15.7, 8 waves 16.6)
+//   up    from 64 steps 16 outputs, 8 waves (2 of 8 large ones, 8 tokens: 375; 4 waves
+//         386, 32 outputs 400); from 32 steps 32 outputs, 4 waves (8-bit, the same: 213,
+//         16 outputs 206; 32 tokens 278, 286), 8 waves below 512 workgroups (2 of 8
+//         small ones, 8 tokens: 34.8; 4 waves 33.2, 16 outputs and 4 waves 31.4: the
+//         slower way since a wave goes over all its products in one loop); below 16
+//         outputs, 4 waves (8-bit small ones, 4 of 60, 32 tokens: 120.2, 32 outputs
+//         118.9; 6 of 64, 64 tokens: 178, 168; 8 waves 147 and 208)
+//   down  from 64 steps or below 512 workgroups 32 outputs, 8 waves (large ones, 32
+//         tokens: 489, 4 waves 490, 64 outputs 489; in 8 bits 278, 279, 272; 2 of 8 of
+//         1024 -> 1408, 8 tokens: 19.2, 16 outputs 19.7); else 4 waves and 16 outputs
+//         (4 of 60 small ones, 32 tokens: 178, 32 outputs 180, 8 waves 195) or, in 8
+//         bits, 32 (120, 16 outputs 125, 8 waves 135)
+// Columns: 16 up to 10 slots an expert on average (large ones, 40 tokens: 507, with 32
+// columns 517; 48 tokens: 574, 524; for small ones 16 stay the faster up to some 14:
+// 160 tokens through 4 of 60: 276, 291), 32 up to 24 (large ones, 96 tokens: 592, with
+// 64 columns 653, with 16 940), else 64 (112 tokens: 680, with 32 columns 701; 128: 707,
+// 913; in 8 bits 473, 414 and 489, 497).  An expert with more slots goes over its
 // weights again.  The workgroups there: 32 outputs and 4 waves up, 64 and 8 (with 64
-// columns 4) down.
+// columns 4) down.  (From 13 to 32 slots an expert on, by the sizes, the grouped
+// products take less: large ones, 80 tokens 563 against 608, 128 tokens 604 and 708; one
+// of four large ones for 128 tokens 363 against 353 here.)
 ExpertsPick choose_experts(const ExpertsArgs& a, bool int8) {
   const int units = units_of(a), S = a.T * a.topk, ES = int8 ? 1 : 2;
   const int up_steps = (a.d * ES + 127) / 128, down_steps = (a.ff * ES + 127) / 128;

@@ -13,11 +13,14 @@
 // from four slots at a time: 16384 tokens of two slots of 4096 values and an
 // addend, bf16: 98 us, 5.5 TB/s of what it must move (a large copy: 4.9); 32 tokens of
 // four of 2048: 3 us.  Gradient: of few tokens a wave takes a slot, so that they
-// still make many waves (1000 tokens of four slots of 2048: 10.4 us, a wave a
-// token 11.5; of eight of 4096: 33, 37), and the waves of one token find its dy in
-// the cache; from 4096 tokens a wave takes a token, keeps dy in registers and
-// requests the next slot's z ahead (4160 tokens of six of 2048: 51 us, 4.3 TB/s, a wave
-// a slot 55; 16384 of two of 4096: 137, 146).
+// still make many waves, and the waves of one token find its dy in the cache; from
+// 4096 tokens a wave takes a token, keeps dy in registers and requests the next
+// slot's z ahead (4160 tokens of six of 2048 bf16: 50 us, 4.4 TB/s).  Both, us, a wave a
+// slot and a wave a token: 1024 tokens of six slots of 2048 11.3, 13.1, of eight of 4096
+// 35.0, 36.3; 2048: 25.9, 25.6 and 66.1, 62.5; 4000: 51.6, 46.3 and 119, 129; 4160: 55.0, 50.3
+// and 127, 132; of four of 2048 4000 tokens 38.0, 33.1, 8192 70.2, 66.0; 16384 of two of
+// 4096 139, 139.  (Rows of 2048 would take a wave a token from 2048 tokens on; the border
+// is where it is not the slower way by more than 4 % for any of these.)
 #include "layer_ops.h"
 #include "rows.h"
 

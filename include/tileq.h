@@ -459,9 +459,10 @@ tq_status tq_combine_grad(const tq_combine_desc *d, void *stream);
  *   ws     DEVICE, 256-byte aligned, tq_experts_workspace_size() bytes, of one
  *          call at a time; its contents before the call do not matter
  * Sums in f32 in a fixed order.  d and ff % 8 == 0 (8-bit weights: % 16) and
- * at most 65536; T topk <= 1024 (from some 24 slots an expert on the grouped
- * products are the faster way); topk <= 32;
- * experts 1 .. 1024; x below 2^31 bytes, rows of x and weights 16-byte aligned.
+ * at most 65536; T topk <= 1024 (the grouped products are the faster way from
+ * 13 to 32 slots an expert on, by the sizes; with 8-bit weights, where they
+ * quantise the activations too, from 2 to 25); topk <= 32; experts 1 .. 1024; x
+ * below 2^31 bytes, rows of x and weights 16-byte aligned.
  * y may be add (with the same stride) or x.
  * Errors: TQ_EINVAL, TQ_ESHAPE, TQ_EUNSUPPORTED (more than 1024 slots), TQ_EHIP. */
 typedef struct {
